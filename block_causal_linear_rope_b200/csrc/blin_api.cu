@@ -43,6 +43,14 @@ static blin_status fail(blin_status st, const char *fmt, ...) {
 
 blin_status blin::set_last_error(blin_status st, const char *msg) { return fail(st, "%s", msg); }
 
+blin_status blin::failf(blin_status st, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return st;
+}
+
 static blin_status cuda_fail(cudaError_t e, const char *what) {
     return fail(BLIN_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
@@ -423,6 +431,29 @@ static blin_status check_io(const void *q, const void *k, const void *v, void *o
     return BLIN_OK;
 }
 
+// Element strides of q/k/v (or o) from the caller's layout (NULL: contiguous).
+blin_status blin::get_layout(const blin_layout *l, int B, int H, int N, int d, blin_dtype dt, const char *name,
+                             Layout *out) {
+    if (l == nullptr) {
+        *out = Layout{d, (long long)N * d, (long long)H * N * d};
+        return BLIN_OK;
+    }
+    Layout x{l->token, l->head, l->batch};
+    // a dimension of extent 1 never moves: give it a harmless stride
+    if (H == 1) x.head = x.tok * (long long)std::max(N, 1);
+    if (B == 1) x.batch = std::max(x.tok * (long long)std::max(N, 1), x.head * (long long)H);
+    if (x.tok < d || x.head < d || x.batch < d)
+        return fail(BLIN_ERR_SHAPE, "%s strides (token %lld, head %lld, batch %lld) must each be >= d = %d", name,
+                    l->token, l->head, l->batch, d);
+    const long long es = dt == BLIN_BF16 ? 2 : 4;
+    if ((x.tok * es) % 16 || (x.head * es) % 16 || (x.batch * es) % 16)
+        return fail(BLIN_ERR_ALIGN, "%s strides must be multiples of 16 bytes", name);
+    if (x.tok * es >= (1LL << 40) || x.head * es >= (1LL << 40) || x.batch * es >= (1LL << 40))
+        return fail(BLIN_ERR_SHAPE, "%s strides too large", name);
+    *out = x;
+    return BLIN_OK;
+}
+
 extern "C" {
 
 const char *blin_last_error(void) { return g_err; }
@@ -560,29 +591,6 @@ static blin_status ensure_scratch(blin_state *st, size_t need, cudaStream_t s) {
     if (st->scratch) cudaFreeAsync(st->scratch, s);
     st->scratch = p;
     st->scratch_bytes = need;
-    return BLIN_OK;
-}
-
-// Element strides of q/k/v (or o) from the caller's layout (NULL: contiguous).
-static blin_status get_layout(const blin_layout *l, int B, int H, int N, int d, blin_dtype dt, const char *name,
-                              Layout *out) {
-    if (l == nullptr) {
-        *out = Layout{d, (long long)N * d, (long long)H * N * d};
-        return BLIN_OK;
-    }
-    Layout x{l->token, l->head, l->batch};
-    // a dimension of extent 1 never moves: give it a harmless stride
-    if (H == 1) x.head = x.tok * (long long)std::max(N, 1);
-    if (B == 1) x.batch = std::max(x.tok * (long long)std::max(N, 1), x.head * (long long)H);
-    if (x.tok < d || x.head < d || x.batch < d)
-        return fail(BLIN_ERR_SHAPE, "%s strides (token %lld, head %lld, batch %lld) must each be >= d = %d", name,
-                    l->token, l->head, l->batch, d);
-    const long long es = dt == BLIN_BF16 ? 2 : 4;
-    if ((x.tok * es) % 16 || (x.head * es) % 16 || (x.batch * es) % 16)
-        return fail(BLIN_ERR_ALIGN, "%s strides must be multiples of 16 bytes", name);
-    if (x.tok * es >= (1LL << 40) || x.head * es >= (1LL << 40) || x.batch * es >= (1LL << 40))
-        return fail(BLIN_ERR_SHAPE, "%s strides too large", name);
-    *out = x;
     return BLIN_OK;
 }
 
@@ -770,6 +778,9 @@ blin_status blin_device_status(int *code) {
     e = read_and_clear_watchdog(&c);
     if (e != cudaSuccess) return cuda_fail(e, "watchdog read");
     if (code) *code = c;
+    if (c == WD_SLOT_RANGE || c == WD_SLOT_TWICE)
+        return fail(BLIN_ERR_DEVICE, "a row of a decayed-attention call named a state slot that %s (code %d)",
+                    c == WD_SLOT_RANGE ? "does not exist" : "an earlier row of the call named too", c);
     if (c != 0) return fail(BLIN_ERR_DEVICE, "a kernel wait ran out (watchdog code %d)", c);
     return BLIN_OK;
 }

@@ -1,0 +1,198 @@
+// Decayed linear attention: argument checks, the split of a prompt into
+// segments, and the launches of blin_decay_prefill and blin_decay_step.
+#include <algorithm>
+#include <cmath>
+
+#include "kern_decay.cuh"
+
+namespace blin {
+
+// Raises a kernel's dynamic shared-memory limit (once per context and kernel).
+template <auto Kernel>
+static cudaError_t allow_smem(int bytes) {
+    static ContextCache<int> done;
+    const unsigned long long ctx = current_context_id();
+    int have = 0;
+    if (done.get(ctx, &have) && have >= bytes) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.put(ctx, bytes);
+    return e;
+}
+
+template <int D, typename T>
+static cudaError_t simt(const DecayArgs &a, cudaStream_t s) {
+    constexpr int smem = SimtCfg<D>::BYTES;
+    cudaError_t e = cudaSuccess;
+    if (a.nseg > 1) {
+        if ((e = allow_smem<decay_simt_kernel<D, T, true>>(smem)) != cudaSuccess) return e;
+        decay_simt_kernel<D, T, true><<<(unsigned)(a.B * a.H * (a.nseg - 1)), 256, smem, s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        note_launch();
+    }
+    if ((e = allow_smem<decay_simt_kernel<D, T, false>>(smem)) != cudaSuccess) return e;
+    decay_simt_kernel<D, T, false><<<(unsigned)(a.B * a.H * a.nseg), 256, smem, s>>>(a);
+    if ((e = cudaGetLastError()) == cudaSuccess) note_launch();
+    return e;
+}
+
+cudaError_t launch_decay_simt(const DecayArgs &a, int d, bool bf16, cudaStream_t s) {
+    switch (d) {
+        case 32: return bf16 ? simt<32, __nv_bfloat16>(a, s) : simt<32, float>(a, s);
+        case 64: return bf16 ? simt<64, __nv_bfloat16>(a, s) : simt<64, float>(a, s);
+        default: return bf16 ? simt<128, __nv_bfloat16>(a, s) : simt<128, float>(a, s);
+    }
+}
+
+template <int D, typename T>
+static cudaError_t step(const DecayArgs &a, cudaStream_t s) {
+    decay_step_kernel<D, T><<<(unsigned)((long long)a.B * a.H * (D / 32)), D, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) note_launch();
+    return e;
+}
+
+cudaError_t launch_decay_step(const DecayArgs &a, int d, bool bf16, cudaStream_t s) {
+    switch (d) {
+        case 32: return bf16 ? step<32, __nv_bfloat16>(a, s) : step<32, float>(a, s);
+        case 64: return bf16 ? step<64, __nv_bfloat16>(a, s) : step<64, float>(a, s);
+        default: return bf16 ? step<128, __nv_bfloat16>(a, s) : step<128, float>(a, s);
+    }
+}
+
+}  // namespace blin
+
+using namespace blin;
+
+static bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Segments of a prompt.  A launch runs its units in waves over the SMs, so its
+// time goes as waves x chunks of a segment; the first launch of a split prompt
+// (states only) costs about half as much per chunk as the second.  The split
+// with the smallest sum is taken, from sizes alone.
+static constexpr int kSms = 148, kMaxSegments = 32;
+struct Split {
+    int nseg, seg;
+};
+static Split split_prompt(long long heads, int N, int chunk, int resident) {
+    const int nc = std::max(1, (N + chunk - 1) / chunk);
+    const long long slots = (long long)kSms * resident;
+    Split best{1, nc * chunk};
+    double cost = 0;
+    for (int s = 1; s <= std::min(nc, kMaxSegments); ++s) {
+        const int len = (nc + s - 1) / s, n = (nc + len - 1) / len;
+        if (n != s || heads * n >= (1LL << 31)) continue;
+        const double waves = (double)((heads * n + slots - 1) / slots), first = (double)((heads * (n - 1) + slots - 1) / slots);
+        const double t = waves * (len + 2 + 0.25 * (n - 1)) + first * (0.5 * len + 3);
+        if (s == 1 || t < cost) {
+            cost = t;
+            best = Split{n, len * chunk};
+        }
+    }
+    return best;
+}
+
+static Split split_of(int B, int H, int N, int d, blin_dtype dt) {
+    (void)dt;
+    return split_prompt((long long)B * H, N, kSimtChunk, d == 128 ? 1 : d == 64 ? 2 : 4);
+}
+
+static size_t workspace_of(const Split &sp, int B, int H, int d) {
+    return sp.nseg > 1 ? sizeof(float) * (size_t)B * H * sp.nseg * d * d : 16;
+}
+
+static blin_status check_shape(int B, int H, int N, int d, blin_dtype dt) {
+    if (B < 1 || H < 1 || N < 0) return failf(BLIN_ERR_INVALID_ARG, "B and H must be >= 1 and N >= 0 (got %d, %d, %d)", B, H, N);
+    if (d != 32 && d != 64 && d != 128) return failf(BLIN_ERR_SHAPE, "head dim d must be 32, 64 or 128 (got %d)", d);
+    if (dt != BLIN_F32 && dt != BLIN_BF16) return failf(BLIN_ERR_DTYPE, "unknown dtype %d", (int)dt);
+    if ((long long)B * H >= (1LL << 24) || N >= (1 << 30))
+        return failf(BLIN_ERR_SHAPE, "problem too large (B*H = %lld, N = %d)", (long long)B * H, N);
+    return BLIN_OK;
+}
+
+// Everything a prefill and a step check alike; fills the call's arguments.
+static blin_status check_call(DecayArgs &a, const void *q, const void *k, const void *v, void *o, blin_dtype dt, int B,
+                              int H, int N, int d, const float *log_decay, float scale, const blin_decay_layouts *lay,
+                              float *S, int slots, const int *slot_of) {
+    blin_status rc = check_shape(B, H, N, d, dt);
+    if (rc != BLIN_OK) return rc;
+    if (q == nullptr || k == nullptr || v == nullptr || o == nullptr || log_decay == nullptr)
+        return failf(BLIN_ERR_INVALID_ARG, "q, k, v, o and log_decay must be non-NULL device pointers");
+    if (!std::isfinite(scale)) return failf(BLIN_ERR_INVALID_ARG, "scale must be finite");
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(S, 16))
+        return failf(BLIN_ERR_ALIGN, "q, k, v, o and S must be 16-byte aligned");
+    if (!aligned(log_decay, 4) || !aligned(slot_of, 4))
+        return failf(BLIN_ERR_ALIGN, "log_decay, lengths and slot_of_row must be 4-byte aligned");
+    if (S != nullptr && slots < 1) return failf(BLIN_ERR_STATE, "slots must be >= 1 (got %d)", slots);
+    if (S != nullptr && slot_of == nullptr && slots != B)
+        return failf(BLIN_ERR_STATE, "without slot_of_row the pool holds one slot per row: slots = %d, B = %d", slots, B);
+    if (S == nullptr && slot_of != nullptr) return failf(BLIN_ERR_STATE, "slot_of_row needs a state pool");
+    if (static_cast<const void *>(o) == q || static_cast<const void *>(o) == k || static_cast<const void *>(o) == v)
+        return failf(BLIN_ERR_INVALID_ARG, "o must not overlap q, k or v");
+    a = DecayArgs{};
+    const char *name[4] = {"q", "k", "v", "o"};
+    Layout *to[4] = {&a.lq, &a.lk, &a.lv, &a.lo};
+    for (int i = 0; i < 4; ++i) {
+        blin_layout l;
+        if (lay) {
+            l = (&lay->q)[i];
+            if (N <= 1) l.token = d;  // a single token never moves
+        }
+        if ((rc = get_layout(lay ? &l : nullptr, B, H, N, d, dt, name[i], to[i])) != BLIN_OK) return rc;
+    }
+    a.q = q, a.k = k, a.v = v, a.o = o;
+    a.B = B, a.H = H, a.N = N;
+    a.log_decay = log_decay;
+    a.scale = scale;
+    a.S = S;
+    a.slots = slots;
+    a.slot_of = slot_of;
+    return BLIN_OK;
+}
+
+static blin_status launched(cudaError_t e, const char *what) {
+    return e == cudaSuccess ? BLIN_OK : failf(BLIN_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+extern "C" {
+
+size_t blin_decay_workspace_size(int B, int H, int N, int d, blin_dtype dt) {
+    if (check_shape(B, H, N, d, dt) != BLIN_OK) return 0;
+    return workspace_of(split_of(B, H, N, d, dt), B, H, d);
+}
+
+blin_status blin_decay_prefill(const void *q, const void *k, const void *v, void *o, blin_dtype dt, int B, int H, int N,
+                               int d, const float *log_decay, float scale, const blin_decay_layouts *layouts,
+                               const int *lengths, float *S, int slots, const int *slot_of_row, void *workspace,
+                               size_t ws_bytes, blin_stream stream) {
+    const TraceRange trace("blin_decay_prefill");
+    DecayArgs a;
+    blin_status rc = check_call(a, q, k, v, o, dt, B, H, N, d, log_decay, scale, layouts, S, slots, slot_of_row);
+    if (rc != BLIN_OK) return rc;
+    if (!aligned(lengths, 4)) return failf(BLIN_ERR_ALIGN, "log_decay, lengths and slot_of_row must be 4-byte aligned");
+    if (N == 0) return BLIN_OK;
+    const Split sp = split_of(B, H, N, d, dt);
+    const size_t need = workspace_of(sp, B, H, d);
+    if (sp.nseg > 1 && (workspace == nullptr || ws_bytes < need))
+        return failf(BLIN_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace ? ws_bytes : 0, need);
+    if (!aligned(workspace, 16)) return failf(BLIN_ERR_ALIGN, "workspace must be 16-byte aligned");
+    a.lengths = lengths;
+    a.nseg = sp.nseg;
+    a.seg = sp.seg;
+    a.ws = static_cast<float *>(workspace);
+    if ((a.wd = watchdog_ptr()) == nullptr) return failf(BLIN_ERR_CUDA, "no CUDA device");
+    return launched(launch_decay_simt(a, d, dt == BLIN_BF16, static_cast<cudaStream_t>(stream)), "decayed attention launch");
+}
+
+blin_status blin_decay_step(const void *q, const void *k, const void *v, void *o, blin_dtype dt, int B, int H, int d,
+                            const float *log_decay, float scale, const blin_decay_layouts *layouts, float *S, int slots,
+                            const int *slot_of_row, blin_stream stream) {
+    const TraceRange trace("blin_decay_step");
+    DecayArgs a;
+    if (S == nullptr) return failf(BLIN_ERR_INVALID_ARG, "a step needs a state pool");
+    const blin_status rc = check_call(a, q, k, v, o, dt, B, H, 1, d, log_decay, scale, layouts, S, slots, slot_of_row);
+    if (rc != BLIN_OK) return rc;
+    if ((a.wd = watchdog_ptr()) == nullptr) return failf(BLIN_ERR_CUDA, "no CUDA device");
+    return launched(launch_decay_step(a, d, dt == BLIN_BF16, static_cast<cudaStream_t>(stream)), "decay step launch");
+}
+
+}  // extern "C"

@@ -101,6 +101,8 @@ enum WatchdogCode : int {
     WD_P2_INFO = 17,    // pass-2 tile record ring
     WD_P2_PREFIX = 18,  // pass-2 producer: a head block's prefix state never became ready
     WD_P2_DRAIN = 19,   // pass-2 final MMA drain
+    WD_SLOT_RANGE = 64, // decayed attention: a row names a pool slot that does not exist
+    WD_SLOT_TWICE = 65, // decayed attention: two rows of one call name the same slot
 };
 
 // Launchers (all enqueue on `s`; return the launch's cudaError_t).
@@ -123,7 +125,8 @@ cudaError_t launch_partial_tc(const KGeom &g, int d, bool fp4, const CUtensorMap
                               cudaStream_t s);
 cudaError_t launch_output_tc(const KGeom &g, int d, bool fp4, const CUtensorMap &mq, void *o, cudaStream_t s);
 
-// Device watchdog access.
+// Device watchdog access: the current context's word, and a read that clears it.
+int *watchdog_ptr();
 cudaError_t read_and_clear_watchdog(int *code);
 
 // Unique id of the calling thread's current CUDA context (0 if none or the
@@ -167,6 +170,12 @@ struct ContextCache {
 
 // Records `msg` as this thread's blin_last_error() text and returns `st`.
 blin_status set_last_error(blin_status st, const char *msg);
+// The same with a format.
+blin_status failf(blin_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+
+// Element strides of a [B][H][N][d] operand from the caller's layout (NULL:
+// contiguous), checked against blin_layout's rules.
+blin_status get_layout(const blin_layout *l, int B, int H, int N, int d, blin_dtype dt, const char *name, Layout *out);
 
 // Counts one kernel launch in blin_launch_count().
 void note_launch();

@@ -25,7 +25,7 @@ cudaError_t read_and_clear_watchdog(int *code) {
     return cudaMemcpyToSymbol(g_watchdog, &zero, sizeof(int));
 }
 
-static int *watchdog_ptr() {
+int *watchdog_ptr() {
     // Address of the current context's watchdog word (a module's device
     // variables exist once per context).
     static ContextCache<int *> cache;

@@ -1,0 +1,98 @@
+// Shared declarations of the decayed linear attention (blin_decay_*): the
+// arguments of one call, the decay arithmetic, and the launchers.
+//
+// A prompt is cut into `nseg` segments of whole chunks.  With one segment a CTA
+// walks a head's prompt from its cached state to its end.  With more, a first
+// launch reduces every segment but the last to its local state (what its tokens
+// add to a zero state), and a second one walks the segments side by side, each
+// from the sum of the states before it:
+//   S_in(s) = g^{start_s} S_0 + sum_{s' < s} g^{start_s - end_s'} local(s').
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "blin_internal.cuh"
+
+namespace blin {
+
+struct DecayArgs {
+    const void *q, *k, *v;
+    void *o;
+    Layout lq, lk, lv, lo;
+    int B, H, N;
+    const float *log_decay;  // [H]
+    float scale;
+    const int *lengths;  // [B] or NULL
+    float *S;            // [slots][H][d][d] or NULL
+    int slots;
+    const int *slot_of;  // [B] or NULL
+    int nseg, seg;       // segments of a prompt and tokens per segment (whole chunks)
+    float *ws;           // nseg > 1: [B*H][nseg][d*d]: the entering state, then local(0 .. nseg - 2)
+    int *wd;
+};
+
+// A head's log decay as the kernels use it: at most 0, NaN where the caller's
+// entry is positive or NaN.  The floor keeps -inf * 0 tokens at a power of 1;
+// exp(-10000 n) is 0 in fp32 for every n >= 1.
+__device__ __forceinline__ float decay_log(const float *log_decay, int h) {
+    const float x = __ldg(log_decay + h);
+    return x <= 0.f ? fmaxf(x, -1e4f) : __int_as_float(0x7fc00000);
+}
+
+// g^n = exp(lg * n).  The product's rounding error is recovered by an FMA and
+// applied to first order: the exponent of a far token is exact to fp32, where
+// expf(lg * n) alone would lose |lg n| * 2^-24.
+__device__ __forceinline__ float decay_pow(float lg, float n) {
+    const float p = lg * n;
+    if (!(p > -150.f)) return p <= -150.f ? 0.f : p;  // underflow, or NaN
+    const float e = expf(p);
+    return fmaf(e, fmaf(lg, n, -p), e);
+}
+
+// One state element decayed by g = e^lgn: S * g as S + S (g - 1) while g is near
+// 1, where rounding g itself would be repeated at every step and add up.
+struct DecayMul {
+    float m;
+    bool near;
+    __device__ __forceinline__ DecayMul(float lg, float n) {
+        const float p = lg * n;
+        near = p > -0.5f;
+        if (near) {
+            const float e = expm1f(p);
+            m = fmaf(e + 1.f, fmaf(lg, n, -p), e);
+        } else {
+            m = decay_pow(lg, n);
+        }
+    }
+    __device__ __forceinline__ float operator()(float s) const { return near ? fmaf(s, m, s) : s * m; }
+};
+
+// The pool slot of batch row b, -1 when the row is idle (all threads of the
+// block call it).  An entry out of range, or one that an earlier row has, makes
+// the row idle and is recorded in the watchdog word.
+__device__ __forceinline__ int decay_slot(const DecayArgs &a, int b) {
+    if (a.slot_of == nullptr) return b;
+    const int s = __ldg(a.slot_of + b);
+    int twice = 0;
+    if (s >= 0 && s < a.slots)
+        for (int i = threadIdx.x; i < b; i += blockDim.x) twice |= __ldg(a.slot_of + i) == s;
+    twice = __syncthreads_or(twice);
+    if (s < 0) return -1;
+    if (s >= a.slots || twice) {
+        if (threadIdx.x == 0) atomicCAS(a.wd, 0, s >= a.slots ? WD_SLOT_RANGE : WD_SLOT_TWICE);
+        return -1;
+    }
+    return s;
+}
+
+// Tokens of batch row b.
+__device__ __forceinline__ int decay_len(const DecayArgs &a, int b) {
+    return a.lengths ? min(max(__ldg(a.lengths + b), 0), a.N) : a.N;
+}
+
+// fp32 CUDA-core path (kern_decay.cuh).
+cudaError_t launch_decay_simt(const DecayArgs &a, int d, bool bf16, cudaStream_t s);
+cudaError_t launch_decay_step(const DecayArgs &a, int d, bool bf16, cudaStream_t s);
+
+}  // namespace blin

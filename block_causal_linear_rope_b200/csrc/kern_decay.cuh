@@ -1,0 +1,349 @@
+// Decayed linear attention on the CUDA cores: prompts in fp32 arithmetic, and
+// the single-token step of both types.
+#pragma once
+
+#include "decay.cuh"
+
+namespace blin {
+
+template <typename T>
+struct Vec16;  // 16 bytes of T widened to fp32
+template <>
+struct Vec16<float> {
+    static constexpr int N = 4;
+    __device__ __forceinline__ static void load(const float *p, float (&f)[4]) {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+    }
+    __device__ __forceinline__ static void store(float *p, const float (&f)[4]) {
+        *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    }
+};
+template <>
+struct Vec16<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ __forceinline__ static void load(const __nv_bfloat16 *p, float (&f)[8]) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ static void store(__nv_bfloat16 *p, const float (&f)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// ---------------------------------------------------------------------------- prompts
+constexpr int kSimtChunk = 64;
+
+template <int D>
+struct SimtCfg {
+    static constexpr int C = kSimtChunk, P = D + 4;  // rows padded by 16 bytes: no bank conflicts on 16-byte reads
+    static constexpr int PP = C + 4;
+    static constexpr int FLOATS = 3 * C * P + C * PP + D * P + 2 * C;
+    static constexpr int BYTES = FLOATS * 4;
+};
+
+template <int V>
+__device__ __forceinline__ void lds_vec(const float *p, float (&f)[V]) {
+    if constexpr (V == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        f[0] = v.x, f[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const float4 v = *reinterpret_cast<const float4 *>(p + 4 * i);
+            f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
+        }
+    }
+}
+
+// One segment of one head, 64 tokens at a time:
+//   o_i = scale (sum_{j <= i} g^{i-j} (q_i . k_j) v_j + g^{i+1} q_i S),
+//   S  <- g^n S + sum_j g^{n-1-j} k_j^T v_j.
+// 16 x 16 threads hold a 4 x 4 tile of the scores, 4 x D/16 of the outputs and
+// D/16 x D/16 of the state; the state's fp32 values stay in registers and a copy
+// in shared memory feeds the products.  STATES: local states only (phase 1).
+template <int D, typename T, bool STATES>
+__global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
+    using Cfg = SimtCfg<D>;
+    constexpr int C = Cfg::C, P = Cfg::P, PP = Cfg::PP, W = D / 16, VN = Vec16<T>::N;
+    extern __shared__ float4 smem4[];
+    float *sq = reinterpret_cast<float *>(smem4), *sk = sq + C * P, *sv = sk + C * P, *sp = sv + C * P,
+          *ss = sp + C * PP, *pw = ss + D * P;  // pw[n] = g^n, n <= C
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int per = STATES ? a.nseg - 1 : a.nseg;
+    const int bh = blockIdx.x / per, seg = blockIdx.x - bh * per;
+    const int b = bh / a.H, h = bh - b * a.H;
+    const int slot = decay_slot(a, b);
+    const int L = slot < 0 ? 0 : decay_len(a, b);
+    const int begin = seg * a.seg, end = min(begin + a.seg, L);
+    const float lg = decay_log(a.log_decay, h);
+    float *wsp = a.ws + (size_t)bh * a.nseg * D * D;
+    float *pool = a.S && slot >= 0 ? a.S + ((size_t)slot * a.H + h) * D * D : nullptr;
+    if (tid <= C) pw[tid] = decay_pow(lg, (float)tid);
+    // column of the w-th value of this thread's W columns (16-byte pieces 64 columns apart)
+    auto col = [&](int w) { return W <= 4 ? tx * W + w : 64 * (w >> 2) + 4 * tx + (w & 3); };
+    float st[W][W];  // state rows ty * W + r, columns col(w)
+#pragma unroll
+    for (int r = 0; r < W; ++r)
+#pragma unroll
+        for (int w = 0; w < W; ++w) st[r][w] = 0.f;
+    if (STATES) {
+        if (seg == 0)  // the second launch may overwrite the pool while others still read the entering state
+            for (int i = tid; i < D * D / 4; i += 256)
+                reinterpret_cast<float4 *>(wsp)[i] =
+                    pool ? reinterpret_cast<const float4 *>(pool)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+    } else if (begin < L) {
+        if (a.nseg == 1) {
+            if (pool)
+#pragma unroll
+                for (int r = 0; r < W; ++r)
+#pragma unroll
+                    for (int w = 0; w < W; ++w) st[r][w] = pool[(ty * W + r) * D + col(w)];
+        } else {
+            for (int s = 0; s <= seg; ++s) {
+                const float f = decay_pow(lg, (float)(begin - s * a.seg));
+#pragma unroll
+                for (int r = 0; r < W; ++r)
+#pragma unroll
+                    for (int w = 0; w < W; ++w)
+                        st[r][w] = fmaf(f, wsp[(size_t)s * D * D + (ty * W + r) * D + col(w)], st[r][w]);
+            }
+        }
+    }
+    const T *qp = static_cast<const T *>(a.q) + b * a.lq.batch + h * a.lq.head;
+    const T *kp = static_cast<const T *>(a.k) + b * a.lk.batch + h * a.lk.head;
+    const T *vp = static_cast<const T *>(a.v) + b * a.lv.batch + h * a.lv.head;
+    T *op = static_cast<T *>(a.o) + b * a.lo.batch + h * a.lo.head;
+    const DecayMul whole(lg, (float)C);
+    for (int n0 = begin; n0 < end; n0 += C) {
+        const int n = min(C, end - n0);  // tokens of this chunk
+        __syncthreads();
+        for (int i = tid; i < C * (D / VN); i += 256) {
+            const int r = i / (D / VN), c = (i - r * (D / VN)) * VN;
+            float f[VN];
+            auto put = [&](float *dst) {
+#pragma unroll
+                for (int u = 0; u < VN; u += 4)
+                    *reinterpret_cast<float4 *>(dst + r * P + c + u) = make_float4(f[u], f[u + 1], f[u + 2], f[u + 3]);
+            };
+            auto get = [&](const T *src, long long tok) {
+                if (r < n) Vec16<T>::load(src + (long long)(n0 + r) * tok + c, f);
+                else
+#pragma unroll
+                    for (int u = 0; u < VN; ++u) f[u] = 0.f;
+            };
+            get(kp, a.lk.tok), put(sk);
+            get(vp, a.lv.tok), put(sv);
+            if (!STATES) get(qp, a.lq.tok), put(sq);
+        }
+        if (!STATES) {
+#pragma unroll
+            for (int r = 0; r < W; ++r)
+#pragma unroll
+                for (int w = 0; w < W; ++w) ss[(ty * W + r) * P + col(w)] = st[r][w];
+        }
+        __syncthreads();
+        if (!STATES) {
+            // a warp's rows end at 8 warp + 7: columns past them are masked and skipped
+            const int jmax = 8 * (tid >> 5) + 8;
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                const int j = tx + 16 * jj;
+                if (16 * jj < jmax) {
+                    for (int c = 0; c < D; c += 4) {
+                        float kv[4];
+                        lds_vec<4>(sk + j * P + c, kv);
+#pragma unroll
+                        for (int ii = 0; ii < 4; ++ii) {
+                            float qv[4];
+                            lds_vec<4>(sq + (4 * ty + ii) * P + c, qv);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) acc[ii] = fmaf(qv[u], kv[u], acc[ii]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int ii = 0; ii < 4; ++ii) {
+                    const int i = 4 * ty + ii;
+                    sp[i * PP + j] = j <= i ? acc[ii] * pw[i - j] : 0.f;
+                }
+            }
+            __syncthreads();
+            float out[4][W], in[4][W];
+#pragma unroll
+            for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+                for (int w = 0; w < W; ++w) out[ii][w] = in[ii][w] = 0.f;
+            auto product = [&](const float *A, int lda, const float *Bm, int kend, float (&acc)[4][W]) {
+                for (int j = 0; j < kend; j += 4) {
+                    float av[4][4];
+#pragma unroll
+                    for (int ii = 0; ii < 4; ++ii) lds_vec<4>(A + (4 * ty + ii) * lda + j, av[ii]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        float bv[W];
+                        if constexpr (W <= 4) {
+                            lds_vec<W>(Bm + (j + u) * P + tx * W, bv);
+                        } else {
+                            float x[4];
+                            lds_vec<4>(Bm + (j + u) * P + 4 * tx, x);
+                            bv[0] = x[0], bv[1] = x[1], bv[2] = x[2], bv[3] = x[3];
+                            lds_vec<4>(Bm + (j + u) * P + 64 + 4 * tx, x);
+                            bv[4] = x[0], bv[5] = x[1], bv[6] = x[2], bv[7] = x[3];
+                        }
+#pragma unroll
+                        for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+                            for (int w = 0; w < W; ++w) acc[ii][w] = fmaf(av[ii][u], bv[w], acc[ii][w]);
+                    }
+                }
+            };
+            product(sp, PP, sv, jmax, out);
+            product(sq, P, ss, D, in);
+#pragma unroll
+            for (int ii = 0; ii < 4; ++ii) {
+                const int i = 4 * ty + ii;
+                if (i < n) {
+                    T *dst = op + (long long)(n0 + i) * a.lo.tok;
+                    const float f = pw[i + 1];
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        const float x = a.scale * fmaf(f, in[ii][w], out[ii][w]);
+                        if constexpr (sizeof(T) == 2) dst[col(w)] = __float2bfloat16_rn(x);
+                        else dst[col(w)] = x;
+                    }
+                }
+            }
+        }
+        // state: the chunk's decay, then its tokens
+        const DecayMul mul = n == C ? whole : DecayMul(lg, (float)n);
+#pragma unroll
+        for (int r = 0; r < W; ++r)
+#pragma unroll
+            for (int w = 0; w < W; ++w) st[r][w] = mul(st[r][w]);
+        for (int j = 0; j < n; ++j) {
+            float kv[W], vv[W];
+            if constexpr (W <= 4) {
+                lds_vec<W>(sk + j * P + ty * W, kv);
+                lds_vec<W>(sv + j * P + tx * W, vv);
+            } else {
+                lds_vec<W>(sk + j * P + ty * W, kv);
+                float x[4];
+                lds_vec<4>(sv + j * P + 4 * tx, x);
+                vv[0] = x[0], vv[1] = x[1], vv[2] = x[2], vv[3] = x[3];
+                lds_vec<4>(sv + j * P + 64 + 4 * tx, x);
+                vv[4] = x[0], vv[5] = x[1], vv[6] = x[2], vv[7] = x[3];
+            }
+            const float f = pw[n - 1 - j];
+#pragma unroll
+            for (int w = 0; w < W; ++w) vv[w] *= f;
+#pragma unroll
+            for (int r = 0; r < W; ++r)
+#pragma unroll
+                for (int w = 0; w < W; ++w) st[r][w] = fmaf(kv[r], vv[w], st[r][w]);
+        }
+    }
+    if (STATES) {
+        float *dst = wsp + (size_t)(seg + 1) * D * D;
+#pragma unroll
+        for (int r = 0; r < W; ++r)
+#pragma unroll
+            for (int w = 0; w < W; ++w) dst[(ty * W + r) * D + col(w)] = st[r][w];
+        return;
+    }
+    if (pool && begin < L && end == L) {
+#pragma unroll
+        for (int r = 0; r < W; ++r)
+#pragma unroll
+            for (int w = 0; w < W; ++w) pool[(ty * W + r) * D + col(w)] = st[r][w];
+    }
+    // rows past the prompt's end are zeros
+    const float zero[VN] = {};
+    const int z0 = max(begin, L), z1 = min(begin + a.seg, a.N);
+    for (long long i = tid; i < (long long)(z1 - z0) * (D / VN); i += 256) {
+        const int r = (int)(i / (D / VN)), c = (int)(i - (long long)r * (D / VN)) * VN;
+        Vec16<T>::store(op + (long long)(z0 + r) * a.lo.tok + c, zero);
+    }
+}
+
+// ---------------------------------------------------------------------------- one token
+// 32 columns of one head's state per CTA, 8 rows of 4 columns per thread: the
+// whole piece is in flight at once, each element is read and written once, and
+// splitting by columns leaves nothing to add up between CTAs.  Bound: HBM (8 d^2
+// bytes per head).
+template <int D, typename T>
+__global__ void __launch_bounds__(D) decay_step_kernel(const DecayArgs a) {
+    constexpr int RG = D / 8;  // row groups: thread rows rg + RG * r
+    __shared__ float4 part[D / 32][8];
+    const int tid = threadIdx.x, cx = tid & 7, rg = tid >> 3;
+    const long long u = blockIdx.x;
+    const int bh = (int)(u / (D / 32)), cg = (int)(u - (long long)bh * (D / 32));
+    const int b = bh / a.H, h = bh - b * a.H;
+    const int c0 = 32 * cg + 4 * cx;
+    // the state's loads go out before the check for repeated slots: an entry in range is safe to read
+    int s = a.slot_of ? __ldg(a.slot_of + b) : b;
+    const bool in = s >= 0 && s < a.slots;
+    float *sp = a.S + ((size_t)(in ? s : 0) * a.H + h) * D * D + c0;
+    float4 st[8];
+    if (in)
+#pragma unroll
+        for (int r = 0; r < 8; ++r) st[r] = *reinterpret_cast<const float4 *>(sp + (rg + RG * r) * D);
+    s = decay_slot(a, b);
+    T *op = static_cast<T *>(a.o) + b * a.lo.batch + h * a.lo.head + c0;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    if (s >= 0) {
+        const T *qp = static_cast<const T *>(a.q) + b * a.lq.batch + h * a.lq.head;
+        const T *kp = static_cast<const T *>(a.k) + b * a.lk.batch + h * a.lk.head;
+        const T *vp = static_cast<const T *>(a.v) + b * a.lv.batch + h * a.lv.head + c0;
+        const DecayMul mul(decay_log(a.log_decay, h), 1.f);
+        float v[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v[w] = static_cast<float>(vp[w]);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const int i = rg + RG * r;
+            const float k = static_cast<float>(kp[i]), q = static_cast<float>(qp[i]);
+            float x[4] = {st[r].x, st[r].y, st[r].z, st[r].w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                x[w] = fmaf(k, v[w], mul(x[w]));
+                acc[w] = fmaf(q, x[w], acc[w]);
+            }
+            *reinterpret_cast<float4 *>(sp + i * D) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+    }
+    // row groups: the four of a warp, then the warps
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        acc[w] += __shfl_xor_sync(~0u, acc[w], 8);
+        acc[w] += __shfl_xor_sync(~0u, acc[w], 16);
+    }
+    if ((tid & 31) < 8) part[tid >> 5][cx] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    __syncthreads();
+    if (tid < 8) {
+        float4 t = part[0][tid];
+#pragma unroll
+        for (int w = 1; w < D / 32; ++w) {
+            const float4 x = part[w][tid];
+            t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+        }
+        op[0] = static_cast<T>(a.scale * t.x);
+        op[1] = static_cast<T>(a.scale * t.y);
+        op[2] = static_cast<T>(a.scale * t.z);
+        op[3] = static_cast<T>(a.scale * t.w);
+    }
+}
+
+}  // namespace blin

@@ -69,7 +69,7 @@ typedef enum {
     BLIN_ERR_WORKSPACE = -5,   /* workspace missing or too small; state scratch that would grow during capture */
     BLIN_ERR_STATE = -6,       /* freed/foreign state, B/H/d mismatch, wrong device, wrong byte count */
     BLIN_ERR_CUDA = -7,        /* a CUDA runtime/driver call failed */
-    BLIN_ERR_DEVICE = -8       /* a kernel's bounded wait ran out (see blin_device_status) */
+    BLIN_ERR_DEVICE = -8       /* a kernel's bounded wait ran out, or a bad slot (see blin_device_status) */
 } blin_status;
 
 typedef enum { BLIN_F32 = 0, BLIN_BF16 = 1 } blin_dtype;
@@ -293,6 +293,94 @@ BLIN_API size_t blin_tconv_state_bytes(const blin_tconv_state *st);
 BLIN_API blin_status blin_tconv(const void *x, const float *taps, const float *bias, void *y, blin_dtype dt, int B,
                                 int C, const blin_geom *g, blin_tconv_state *st, int commit, blin_stream stream);
 
+/* ---------------------------------------------------------------- decayed linear attention */
+
+/* Token-causal linear attention with one decay per head, for prompts and single
+ * tokens (the method on the SANA-Video pages has no decay; this stands beside
+ * its block-causal form for sequences that forget):
+ *   S_n = g_h S_{n-1} + k_n^T v_n          (d x d, fp32)      g_h = exp(log_decay[h])
+ *   o_n = scale * q_n S_n
+ * There is no feature map and no denominator.  d is 32, 64 or 128.
+ *   log_decay  device fp32 [H], each <= 0 (0: no decay; -inf: only the token
+ *              itself).  A positive or NaN entry makes its head's outputs and
+ *              states NaN.
+ *   S          device fp32 [slots][H][d][d], 16-byte aligned, owned by the
+ *              caller: a pool of states (row = key feature, column = value
+ *              feature).  Nothing else is kept between calls.
+ *   slot_of_row  device int32 [B]: the pool slot of each batch row; NULL: row b
+ *              uses slot b (then slots must equal B).  A negative entry marks
+ *              an idle row: its outputs are zeros and no state is touched.  An
+ *              entry >= slots, and one that an earlier row of the call names
+ *              too, is treated as idle and recorded for blin_device_status.
+ *   layouts    element strides of q, k, v and o, NULL: contiguous.  Rules as for
+ *              blin_layout; q, k and v may differ.
+ * o must not overlap q, k, v or S. */
+typedef struct {
+    blin_layout q, k, v, o;
+} blin_decay_layouts;
+
+/* Workspace bytes of blin_decay_prefill for this shape (0 on invalid input; at
+ * most 16: none is needed and the workspace may be NULL). */
+BLIN_API size_t blin_decay_workspace_size(int B, int H, int N, int d, blin_dtype dt);
+
+/* A batch of prompts.
+ *   q, k, v, o  device [B][H][N][d] of dtype dt
+ *   lengths     device int32 [B]: tokens of each row, NULL: N each; values are
+ *               clamped to [0, N].  o's rows from a row's length on are zeros,
+ *               and what q, k and v hold there is never used (it may be NaN).
+ *   S           NULL: every row starts from zero and no state is kept
+ *               (slot_of_row must be NULL).  Otherwise each row starts from its
+ *               slot's state and leaves its state after its last token there (a
+ *               row of length 0 leaves it as it was).  A new sequence's slot is
+ *               zeroed by the caller.
+ *   workspace   device scratch of at least blin_decay_workspace_size bytes,
+ *               16-byte aligned; calls that may run at the same time need
+ *               separate workspaces.
+ * N = 0 is valid and does nothing.  Prompts may be split into several calls.
+ * The sums are taken in chunks of 64 or 128 tokens: an infinity or NaN in a
+ * given token may also reach earlier rows of its chunk. */
+BLIN_API blin_status blin_decay_prefill(const void *q, const void *k, const void *v, void *o, blin_dtype dt, int B,
+                                        int H, int N, int d, const float *log_decay, float scale,
+                                        const blin_decay_layouts *layouts, const int *lengths, float *S, int slots,
+                                        const int *slot_of_row, void *workspace, size_t ws_bytes,
+                                        blin_stream stream);
+
+/* One token per batch row: q, k, v, o are [B][H][d] (the token stride of
+ * `layouts` is not used).  Reads and updates each served row's state. */
+BLIN_API blin_status blin_decay_step(const void *q, const void *k, const void *v, void *o, blin_dtype dt, int B,
+                                     int H, int d, const float *log_decay, float scale,
+                                     const blin_decay_layouts *layouts, float *S, int slots, const int *slot_of_row,
+                                     blin_stream stream);
+
+/* ---------------------------------------------------------------- rotary embedding */
+
+/* The 3D RoPE of the attention above as an operator of its own, for q and k of
+ * another attention.  Sections, pairs and angles are those at the top of this
+ * file (consecutive t, y, x sections, interleaved pairs, p * theta^(-2j/d_axis),
+ * angles in double precision), but rope_split may sum to less than d: features
+ * from the sum on are copied.
+ *   q, q_out  device [B][Hq][N][d] of dtype dt; k, k_out [B][Hk][N][d], both
+ *             NULL to rotate q alone.  d a multiple of 8, at most 256.  An output
+ *             may be its own input (same address and strides: in place); other
+ *             overlaps are not allowed.
+ *   g         rope_split and theta; with positions == NULL also T, Hgt and Wid,
+ *             N = T*Hgt*Wid in the grid order of this file (the other fields are
+ *             not used)
+ *   t0        absolute index of the grid's first frame (>= 0)
+ *   positions device int32 (t, y, x) of each token, [B][N][3] (shared = 0) or
+ *             [N][3] for all batch rows (shared = 1), 4-byte aligned; any values
+ *   inverse   1: rotate by the negative angles, which undoes the rotation and
+ *             takes an output's gradient to its input's
+ *   layouts   element strides of q, q_out, k, k_out (blin_layout's rules); NULL:
+ *             contiguous */
+typedef struct {
+    blin_layout q, q_out, k, k_out;
+} blin_rope_layouts;
+
+BLIN_API blin_status blin_rope(const void *q, void *q_out, int Hq, const void *k, void *k_out, int Hk, blin_dtype dt,
+                               int B, int N, int d, const blin_geom *g, int t0, const int *positions, int shared,
+                               int inverse, const blin_rope_layouts *layouts, blin_stream stream);
+
 /* ---------------------------------------------------------------- no allocation */
 
 /* blin_prefill for callers that cannot allocate device memory (the method on
@@ -340,7 +428,9 @@ BLIN_API int blin_last_path(void);
 
 /* Read (synchronously) and clear the current device's kernel watchdog word:
  * 0 = no bounded wait ran out since the last call; otherwise a code naming the
- * wait that gave up.  Returns BLIN_ERR_DEVICE when the word was non-zero. */
+ * wait that gave up, or 64 (a pool slot out of range) or 65 (a slot named by two
+ * rows of one call) from the decayed attention.  Returns BLIN_ERR_DEVICE when
+ * the word was non-zero. */
 BLIN_API blin_status blin_device_status(int *code);
 
 /* Per-launch timing (profiling aid).  When `events` is non-NULL, the calling
