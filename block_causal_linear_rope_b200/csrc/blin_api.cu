@@ -274,12 +274,12 @@ static EncodeTiledFn encode_fn() {
 }
 
 // 4D view of a bf16 [B][H][N][d] operand with element strides `l`: dimensions
-// (feature, then token and head ordered by stride, then batch), `box_rows`
-// tokens per box, swizzled to the row size (64 B at d = 32, 128 B at d = 64).
-// *swap = 1 when the head dimension comes before the token one.  Tokens past
-// N read as zeros.
-static bool make_map4(CUtensorMap *m, const void *base, const Layout &l, int B, int H, int N, int d, int box_rows,
-                      int *swap) {
+// (feature, then token and head ordered by stride, then batch), boxes of
+// `box_rows` tokens and up to 64 features, swizzled to the box's row size (64 B
+// at d = 32, else 128 B).  *swap = 1 when the head dimension comes before the
+// token one.  Tokens past N read as zeros.
+bool blin::make_map4(CUtensorMap *m, const void *base, const Layout &l, int B, int H, int N, int d, int box_rows,
+                     int *swap) {
     EncodeTiledFn enc = encode_fn();
     if (enc == nullptr) return false;
     const bool sw = l.head < l.tok;
@@ -287,7 +287,7 @@ static bool make_map4(CUtensorMap *m, const void *base, const Layout &l, int B, 
     cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)(sw ? H : N), (cuuint64_t)(sw ? N : H), (cuuint64_t)B};
     cuuint64_t strides[3] = {(cuuint64_t)(sw ? l.head : l.tok) * 2, (cuuint64_t)(sw ? l.tok : l.head) * 2,
                              (cuuint64_t)l.batch * 2};
-    cuuint32_t box[4] = {(cuuint32_t)d, (cuuint32_t)(sw ? 1 : box_rows), (cuuint32_t)(sw ? box_rows : 1), 1};
+    cuuint32_t box[4] = {(cuuint32_t)std::min(d, 64), (cuuint32_t)(sw ? 1 : box_rows), (cuuint32_t)(sw ? box_rows : 1), 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, d == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,

@@ -4,6 +4,7 @@
 #include <cmath>
 
 #include "kern_decay.cuh"
+#include "kern_decay_tc.cuh"
 
 namespace blin {
 
@@ -19,28 +20,49 @@ static cudaError_t allow_smem(int bytes) {
     return e;
 }
 
-template <int D, typename T>
-static cudaError_t simt(const DecayArgs &a, cudaStream_t s) {
-    constexpr int smem = SimtCfg<D>::BYTES;
+// A prompt's launches: with several segments the local states first.
+template <auto States, auto Outputs, typename... Args>
+static cudaError_t launch_prompt(const DecayArgs &a, int states_threads, int states_smem, int threads, int smem,
+                                 cudaStream_t s, const Args &...args) {
     cudaError_t e = cudaSuccess;
     if (a.nseg > 1) {
-        if ((e = allow_smem<decay_simt_kernel<D, T, true>>(smem)) != cudaSuccess) return e;
-        decay_simt_kernel<D, T, true><<<(unsigned)(a.B * a.H * (a.nseg - 1)), 256, smem, s>>>(a);
+        if ((e = allow_smem<States>(states_smem)) != cudaSuccess) return e;
+        States<<<(unsigned)(a.B * a.H * (a.nseg - 1)), states_threads, states_smem, s>>>(args..., a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         note_launch();
     }
-    if ((e = allow_smem<decay_simt_kernel<D, T, false>>(smem)) != cudaSuccess) return e;
-    decay_simt_kernel<D, T, false><<<(unsigned)(a.B * a.H * a.nseg), 256, smem, s>>>(a);
+    if ((e = allow_smem<Outputs>(smem)) != cudaSuccess) return e;
+    Outputs<<<(unsigned)(a.B * a.H * a.nseg), threads, smem, s>>>(args..., a);
     if ((e = cudaGetLastError()) == cudaSuccess) note_launch();
     return e;
 }
 
-cudaError_t launch_decay_simt(const DecayArgs &a, int d, bool bf16, cudaStream_t s) {
-    switch (d) {
-        case 32: return bf16 ? simt<32, __nv_bfloat16>(a, s) : simt<32, float>(a, s);
-        case 64: return bf16 ? simt<64, __nv_bfloat16>(a, s) : simt<64, float>(a, s);
-        default: return bf16 ? simt<128, __nv_bfloat16>(a, s) : simt<128, float>(a, s);
-    }
+template <int D>
+static cudaError_t simt(const DecayArgs &a, cudaStream_t s) {
+    constexpr int smem = SimtCfg<D>::BYTES;
+    return launch_prompt<decay_simt_kernel<D, float, true>, decay_simt_kernel<D, float, false>>(a, 256, smem, 256, smem, s);
+}
+
+cudaError_t launch_decay_simt(const DecayArgs &a, int d, cudaStream_t s) {
+    return d == 32 ? simt<32>(a, s) : d == 64 ? simt<64>(a, s) : simt<128>(a, s);
+}
+
+template <int D>
+static cudaError_t tc(const DecayArgs &a, const DecayMaps &m, cudaStream_t s) {
+    using CS = DecayTc<D, true>;
+    using CO = DecayTc<D, false>;
+    return launch_prompt<decay_tc_kernel<D, true>, decay_tc_kernel<D, false>>(a, CS::THREADS, CS::BYTES, CO::THREADS,
+                                                                             CO::BYTES, s, m);
+}
+
+cudaError_t launch_decay_tc(const DecayArgs &a, int d, cudaStream_t s) {
+    DecayMaps m;
+    if (!make_map4(&m.q, a.q, a.lq, a.B, a.H, a.N, d, 128, &m.swap_q) ||
+        !make_map4(&m.k, a.k, a.lk, a.B, a.H, a.N, d, 128, &m.swap_k) ||
+        !make_map4(&m.v, a.v, a.lv, a.B, a.H, a.N, d, 128, &m.swap_v) ||
+        !make_map4(&m.o, a.o, a.lo, a.B, a.H, a.N, d, 32, &m.swap_o))
+        return cudaErrorInvalidValue;
+    return d == 32 ? tc<32>(a, m, s) : d == 64 ? tc<64>(a, m, s) : tc<128>(a, m, s);
 }
 
 template <int D, typename T>
@@ -92,7 +114,8 @@ static Split split_prompt(long long heads, int N, int chunk, int resident) {
 }
 
 static Split split_of(int B, int H, int N, int d, blin_dtype dt) {
-    (void)dt;
+    // CTAs that share an SM: by shared memory
+    if (dt == BLIN_BF16) return split_prompt((long long)B * H, N, 128, d == 32 ? 2 : 1);
     return split_prompt((long long)B * H, N, kSimtChunk, d == 128 ? 1 : d == 64 ? 2 : 4);
 }
 
@@ -180,7 +203,8 @@ blin_status blin_decay_prefill(const void *q, const void *k, const void *v, void
     a.seg = sp.seg;
     a.ws = static_cast<float *>(workspace);
     if ((a.wd = watchdog_ptr()) == nullptr) return failf(BLIN_ERR_CUDA, "no CUDA device");
-    return launched(launch_decay_simt(a, d, dt == BLIN_BF16, static_cast<cudaStream_t>(stream)), "decayed attention launch");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return launched(dt == BLIN_BF16 ? launch_decay_tc(a, d, s) : launch_decay_simt(a, d, s), "decayed attention launch");
 }
 
 blin_status blin_decay_step(const void *q, const void *k, const void *v, void *o, blin_dtype dt, int B, int H, int d,

@@ -101,6 +101,13 @@ enum WatchdogCode : int {
     WD_P2_INFO = 17,    // pass-2 tile record ring
     WD_P2_PREFIX = 18,  // pass-2 producer: a head block's prefix state never became ready
     WD_P2_DRAIN = 19,   // pass-2 final MMA drain
+    WD_DC_FULL = 32,    // decayed attention: tile landing
+    WD_DC_EMPTY = 33,   // decayed attention: landing slot release
+    WD_DC_VALUE = 34,   // decayed attention: weighted values written / multiplied
+    WD_DC_SCORE = 35,   // decayed attention: scores ready / weighted
+    WD_DC_STATE = 36,   // decayed attention: state product ready / read
+    WD_DC_OUT = 37,     // decayed attention: output ready / read
+    WD_DC_DRAIN = 38,   // decayed attention: final MMA drain
     WD_SLOT_RANGE = 64, // decayed attention: a row names a pool slot that does not exist
     WD_SLOT_TWICE = 65, // decayed attention: two rows of one call name the same slot
 };
@@ -176,6 +183,9 @@ blin_status failf(blin_status st, const char *fmt, ...) __attribute__((format(pr
 // Element strides of a [B][H][N][d] operand from the caller's layout (NULL:
 // contiguous), checked against blin_layout's rules.
 blin_status get_layout(const blin_layout *l, int B, int H, int N, int d, blin_dtype dt, const char *name, Layout *out);
+
+// 4D tensor map of a bf16 [B][H][N][d] operand (see its definition).
+bool make_map4(CUtensorMap *m, const void *base, const Layout &l, int B, int H, int N, int d, int box_rows, int *swap);
 
 // Counts one kernel launch in blin_launch_count().
 void note_launch();

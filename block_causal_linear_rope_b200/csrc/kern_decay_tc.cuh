@@ -1,0 +1,582 @@
+// Decayed linear attention of bf16 prompts on the tensor cores (sm_100a).
+//
+// A CTA walks one segment of one head, 128 tokens at a time.  Per chunk, with
+// i, j the tokens of the chunk, n their number and g the head's decay:
+//   scores   P_ij = g^{i-j} (q_i . k_j) for j <= i, else 0        (128 x 128, K = d)
+//   outputs  o_i  = scale (sum_j P_ij v_j + g^{i+1} q_i S)         (128 x d, K = 128 and K = d)
+//   state    S   <- g^n S + sum_j k_j^T (g^{n-1-j} v_j)            (d x d, K = 128)
+// All four products run on tcgen05.mma with fp32 accumulators in TMEM.
+//
+// Precision.  P and the S that multiplies q are rounded to bf16 (each product's
+// other operand is bf16 already, and so is the result).  The state itself is
+// fp32 and stays in registers from chunk to chunk; the weighted values
+// g^{n-1-j} v_j of its update are split into three bf16 parts (8 + 8 + 8 bits),
+// so that its product carries fp32 accuracy.
+//
+// Roles: a TMA producer thread, an MMA issuing thread, four warps that weight
+// the scores (TMEM -> registers -> P as bf16 over the scores in TMEM), four that
+// weight and split the values (shared memory -> shared memory), and four (d =
+// 128: eight) that own the state and the outputs.  They hand over through
+// mbarriers; every wait is bounded.
+//
+// A state product has only d rows.  Its A operand repeats the d features
+// (leading byte offset 0) up to the 128 lanes, and the lanes of each copy take a
+// share of the columns, so that all 128 threads of a warpgroup update the state.
+#pragma once
+
+#include "decay.cuh"
+#include "tc_util.cuh"
+
+namespace blin {
+
+template <int D, bool STATES>
+struct DecayTc {
+    static constexpr int C = 128;                     // tokens per chunk
+    static constexpr int AW = D == 32 ? 32 : 64;      // features per swizzle atom
+    static constexpr int NAT = D / AW;                // atoms per tile
+    static constexpr int ROWB = 2 * AW;
+    static constexpr int SUB = C * ROWB, TILE = NAT * SUB;
+    static constexpr uint32_t LAYOUT = D == 32 ? 4u : 2u;  // 64B / 128B swizzle
+    static constexpr int TPC = STATES ? 2 : 3;             // tiles landed per chunk: K, (Q,) V
+    static constexpr int NSLOT = D == 32 ? 9 : D == 64 ? 6 : 5;
+    // weighted values: items of IT tokens, three parts each, in a ring of NVB
+    static constexpr int IT = D == 128 ? 16 : 64, NIT = C / IT, NVB = 2;
+    static constexpr int VSUB = IT * ROWB, VPART = NAT * VSUB, VITEM = 3 * VPART;
+    static constexpr int SIMG = 2 * D * D, NSB = D == 128 ? 1 : 2;  // bf16 state images
+    static constexpr int OSTG = STATES || D == 128 ? 0 : TILE;      // output staging (d = 128: in the chunk's Q slot)
+    static constexpr int OFF_V = NSLOT * TILE, OFF_S = OFF_V + NVB * VITEM, OFF_O = OFF_S + (STATES ? 0 : NSB * SIMG);
+    static constexpr int OFF_CTRL = OFF_O + OSTG;
+    static constexpr int NBAR = 2 * NSLOT + 2 * NVB + 9;
+    static constexpr int OFF_PW = OFF_CTRL + 256;  // g^n for n = 0 .. 128, then g^{31 - m} for m < 32
+    static constexpr int BYTES = OFF_PW + 4 * (132 + 32) + 1024;
+    static_assert(8 * NBAR <= 248, "barriers");
+    static_assert(BYTES <= 227 * 1024, "shared memory");
+    // warps
+    static constexpr int XW = STATES ? 0 : 4, TW = 4, UW = D == 128 ? 8 : 4;
+    static constexpr int THREADS = 32 * (XW + TW + UW + 2);
+    // TMEM columns: scores / P, inner and carried outputs, state product (high part | rest, or all of it)
+    static constexpr int KVC = D == 128 ? 128 : 2 * D;
+    static constexpr int T_OA = 128, T_OI = T_OA + D, T_KV = STATES ? 0 : T_OI + D;
+    static constexpr int TCOLS = STATES ? KVC : D == 32 ? 256 : 512;
+    static_assert(T_KV + KVC <= TCOLS, "TMEM columns");
+    static constexpr int NCOL = D == 128 ? 64 : D * D / 128;  // state columns per thread
+};
+
+// Maps and swaps of one call's operands.
+struct DecayMaps {
+    CUtensorMap q, k, v, o;
+    int swap_q, swap_k, swap_v, swap_o;
+};
+
+template <int D, bool STATES>
+struct DecayUnit {
+    using Cf = DecayTc<D, STATES>;
+    const DecayArgs &a;
+    uint8_t *base;
+    uint64_t *bars;
+    volatile int *flag;
+    float *pw, *lead;
+    uint32_t tmem;
+    int b, h, begin, end;  // tokens [begin, end) of batch row b, head h
+    float lg;
+    float *pool, *wsp;
+    int seg;
+
+    // barriers: full/empty of the landing slots, ready/free of the weighted values, then one each
+    enum { B_SFULL, B_PREADY, B_KVFULL, B_KVEMPTY, B_SREADY, B_QSDONE, B_OFULL, B_OEMPTY, B_DRAIN };
+    __device__ uint32_t bar(int i) const { return ptx::smem_u32(bars + i); }
+    __device__ uint32_t full(int s) const { return bar(s); }
+    __device__ uint32_t empty(int s) const { return bar(Cf::NSLOT + s); }
+    __device__ uint32_t vready(int s) const { return bar(2 * Cf::NSLOT + s); }
+    __device__ uint32_t vfree(int s) const { return bar(2 * Cf::NSLOT + Cf::NVB + s); }
+    __device__ uint32_t one(int i) const { return bar(2 * Cf::NSLOT + 2 * Cf::NVB + i); }
+    __device__ uint8_t *slot(int t) const { return base + (t % Cf::NSLOT) * Cf::TILE; }
+    __device__ uint8_t *vbuf(int i) const { return base + Cf::OFF_V + (i % Cf::NVB) * Cf::VITEM; }
+    __device__ uint8_t *sbuf(int c) const { return base + Cf::OFF_S + (c % Cf::NSB) * Cf::SIMG; }
+    // tile numbers of chunk c in landing order
+    __device__ static int tk(int c) { return Cf::TPC * c; }
+    __device__ static int tq(int c) { return Cf::TPC * c + 1; }
+    __device__ static int tv(int c) { return Cf::TPC * c + Cf::TPC - 1; }
+
+    __device__ void init_barriers() const {
+        for (int s = 0; s < Cf::NSLOT; ++s) {
+            ptx::mbar_init(full(s), 1);          // producer (+ bytes)
+            ptx::mbar_init(empty(s), Cf::UW);    // state / output warps
+        }
+        for (int s = 0; s < Cf::NVB; ++s) {
+            ptx::mbar_init(vready(s), Cf::TW);
+            ptx::mbar_init(vfree(s), 1);
+        }
+        ptx::mbar_init(one(B_SFULL), 1);
+        ptx::mbar_init(one(B_PREADY), 4);
+        ptx::mbar_init(one(B_KVFULL), 1);
+        ptx::mbar_init(one(B_KVEMPTY), Cf::UW);
+        ptx::mbar_init(one(B_SREADY), Cf::UW);
+        ptx::mbar_init(one(B_QSDONE), 1);
+        ptx::mbar_init(one(B_OFULL), 1);
+        ptx::mbar_init(one(B_OEMPTY), Cf::UW);
+        ptx::mbar_init(one(B_DRAIN), 1);
+    }
+    // Waits for the phase's completion number `k` (from 0); false: gave up, or another role has.
+    __device__ bool wait(uint32_t br, int k, int code) const {
+        if (ptx::mbar_wait_bounded(br, k & 1, a.wd, code, kWaitLimitNs) && !*flag) return true;
+        *flag = 1;
+        return false;
+    }
+    __device__ int chunks() const { return (end - begin + Cf::C - 1) / Cf::C; }
+    __device__ int tokens(int c) const { return min(Cf::C, end - begin - c * Cf::C); }
+
+    // ------------------------------------------------------------ TMA producer (one thread)
+    __device__ void producer(const DecayMaps &m) const {
+        const uint64_t once = ptx::l2_evict_first();
+        const int nc = chunks();
+        int t = 0;
+        bool ok = true;
+        for (int c = 0; c < nc && ok; ++c) {
+            const int n = begin + c * Cf::C;
+            for (int w = 0; w < Cf::TPC; ++w, ++t) {
+                const int s = t % Cf::NSLOT;
+                if (t >= Cf::NSLOT && !(ok = wait(empty(s), t / Cf::NSLOT - 1, WD_DC_EMPTY))) break;
+                const bool isv = w == Cf::TPC - 1, isk = w == 0;
+                const CUtensorMap *map = isk ? &m.k : isv ? &m.v : &m.q;
+                const MapCoord mc = map_coord(n, h, isk ? m.swap_k : isv ? m.swap_v : m.swap_q);
+                ptx::mbar_arrive_expect_tx(full(s), Cf::TILE);
+#pragma unroll
+                for (int at = 0; at < Cf::NAT; ++at)
+                    ptx::tma_load_4d_hint(ptx::smem_u32(slot(t)) + at * Cf::SUB, map, full(s), at * Cf::AW, mc.y, mc.z, b,
+                                          once);
+            }
+        }
+        // no copy may be in flight when the CTA ends: the last tile of each slot has landed
+        for (int u = max(0, t - Cf::NSLOT); u < t; ++u)
+            ptx::mbar_wait_bounded(full(u % Cf::NSLOT), (u / Cf::NSLOT) & 1, a.wd, WD_DC_FULL, kWaitLimitNs);
+    }
+
+    // ------------------------------------------------------------ MMA issuer (one thread)
+    __device__ void mma() const {
+        constexpr int ROWB = Cf::ROWB, KT = 8 * ROWB;  // bytes of 8 rows
+        const int nc = chunks();
+        for (int c = 0; c < nc; ++c) {
+            if (!wait(full(tk(c) % Cf::NSLOT), tk(c) / Cf::NSLOT, WD_DC_FULL)) break;
+            const uint32_t ka = ptx::smem_u32(slot(tk(c)));
+            uint32_t qa = 0;
+            if constexpr (!STATES) {
+                if (!wait(full(tq(c) % Cf::NSLOT), tq(c) / Cf::NSLOT, WD_DC_FULL)) break;
+                qa = ptx::smem_u32(slot(tq(c)));
+                // the scores' columns were last read by the PV product issued before this one
+                constexpr uint32_t ID = ptx::idesc_bf16_f32(128, 128, 0, 0);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const int at = kk / (Cf::AW / 16), jj = kk % (Cf::AW / 16);
+                    ptx::mma_bf16_ss(tmem, ptx::smem_desc(qa + at * Cf::SUB + 32 * jj, 16, KT, Cf::LAYOUT),
+                                     ptx::smem_desc(ka + at * Cf::SUB + 32 * jj, 16, KT, Cf::LAYOUT), ID, kk > 0);
+                }
+                ptx::mma_commit(one(B_SFULL));
+            }
+            // state product, item by item
+            if (c > 0 && !wait(one(B_KVEMPTY), c - 1, WD_DC_STATE)) break;
+            bool ok = true;
+            for (int it = 0; it < Cf::NIT; ++it) {
+                const int i = c * Cf::NIT + it;
+                if (!(ok = wait(vready(i % Cf::NVB), i / Cf::NVB, WD_DC_VALUE))) break;
+                ptx::tc_fence_after_sync();
+                const uint64_t ad = ptx::smem_desc(ka, D == 128 ? Cf::SUB : 0, KT, Cf::LAYOUT) + it * (Cf::IT / 16) * ROWB;
+                const uint32_t vb = ptx::smem_u32(vbuf(i));
+#pragma unroll
+                for (int kk = 0; kk < Cf::IT / 16; ++kk) {
+                    const uint64_t bo = static_cast<uint64_t>(kk * ROWB);
+                    const uint32_t acc = it > 0 || kk > 0;
+                    if constexpr (D == 128) {  // small parts first
+                        constexpr uint32_t ID = ptx::idesc_bf16_f32(128, 128, 1, 1);
+#pragma unroll
+                        for (int part = 2; part >= 0; --part)
+                            ptx::mma_bf16_ss(tmem + Cf::T_KV, ad + bo,
+                                             ptx::smem_desc(vb + part * Cf::VPART, Cf::VSUB, KT, Cf::LAYOUT) + bo, ID,
+                                             acc | (part < 2));
+                    } else {
+                        // the low part into the middle part's columns, then high | middle
+                        constexpr uint32_t IDL = ptx::idesc_bf16_f32(128, D, 1, 1), IDH = ptx::idesc_bf16_f32(128, 2 * D, 1, 1);
+                        ptx::mma_bf16_ss(tmem + Cf::T_KV, ad + bo, ptx::smem_desc(vb, Cf::VSUB, KT, Cf::LAYOUT) + bo, IDH, acc);
+                        ptx::mma_bf16_ss(tmem + Cf::T_KV + D, ad + bo,
+                                         ptx::smem_desc(vb + 2 * Cf::VPART, Cf::VSUB, KT, Cf::LAYOUT) + bo, IDL, 1u);
+                    }
+                }
+                ptx::mma_commit(vfree(i % Cf::NVB));
+            }
+            if (!ok) break;
+            ptx::mma_commit(one(B_KVFULL));
+            if constexpr (!STATES) {
+                if (!wait(one(B_SREADY), c, WD_DC_STATE)) break;
+                if (c > 0 && !wait(one(B_OEMPTY), c - 1, WD_DC_OUT)) break;
+                if (!wait(full(tv(c) % Cf::NSLOT), tv(c) / Cf::NSLOT, WD_DC_FULL)) break;
+                ptx::tc_fence_after_sync();
+                constexpr uint32_t ID = ptx::idesc_bf16_f32(128, D, 0, 1);
+                const uint64_t sd = ptx::smem_desc(ptx::smem_u32(sbuf(c)), D * ROWB, KT, Cf::LAYOUT);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const int at = kk / (Cf::AW / 16), jj = kk % (Cf::AW / 16);
+                    ptx::mma_bf16_ss(tmem + Cf::T_OI, ptx::smem_desc(qa + at * Cf::SUB + 32 * jj, 16, KT, Cf::LAYOUT),
+                                     sd + static_cast<uint64_t>(kk * ROWB), ID, kk > 0);
+                }
+                if (Cf::NSB == 1) ptx::mma_commit(one(B_QSDONE));
+                if (!wait(one(B_PREADY), c, WD_DC_SCORE)) break;
+                ptx::tc_fence_after_sync();
+                const uint64_t vd = ptx::smem_desc(ptx::smem_u32(slot(tv(c))), Cf::SUB, KT, Cf::LAYOUT);
+#pragma unroll
+                for (int kk = 0; kk < Cf::C / 16; ++kk)
+                    ptx::mma_bf16_ts(tmem + Cf::T_OA, tmem + 8 * kk, vd + static_cast<uint64_t>(kk * ROWB), ID, kk > 0);
+                ptx::mma_commit(one(B_OFULL));
+            }
+        }
+        // every MMA and the arrivals of its commit complete before TMEM is released
+        ptx::mma_commit(one(B_DRAIN));
+        ptx::mbar_wait_bounded(one(B_DRAIN), 0, a.wd, WD_DC_DRAIN, kWaitLimitNs);
+    }
+
+    // ------------------------------------------------------------ score warps (row i per thread)
+    __device__ void scores(int w, int lane) const {
+        const uint32_t row = tmem + (static_cast<uint32_t>(32 * w) << 16);
+        // g^{i-j} = g^{i - 32 blk - 31} * g^{31 - (j - 32 blk)} left of the diagonal block: both powers >= 0
+        float far[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) far[k] = pw[32 * k + 1 + lane];
+        const int nc = chunks();
+        for (int c = 0; c < nc; ++c) {
+            if (!wait(one(B_SFULL), c, WD_DC_SCORE)) break;
+            ptx::tc_fence_after_sync();
+#pragma unroll
+            for (int blk = 0; blk < 4; ++blk) {
+                uint32_t p[16];
+                if (blk <= w) {
+                    uint32_t s0[16], s1[16];
+                    ptx::tmem_ld(row + 32 * blk, s0);
+                    ptx::tmem_ld(row + 32 * blk + 16, s1);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_pin(s0);
+                    ptx::tmem_pin(s1);
+                    if (blk < w) {
+                        const float f = w - blk == 1 ? far[0] : w - blk == 2 ? far[1] : far[2];
+#pragma unroll
+                        for (int m = 0; m < 32; m += 4) {
+                            const float4 l = *reinterpret_cast<const float4 *>(lead + m);
+                            auto s = [&](int x) { return __uint_as_float(x < 16 ? s0[x & 15] : s1[x & 15]); };
+                            p[m / 2] = pack_bf16x2(s(m) * (f * l.x), s(m + 1) * (f * l.y));
+                            p[m / 2 + 1] = pack_bf16x2(s(m + 2) * (f * l.z), s(m + 3) * (f * l.w));
+                        }
+                    } else {
+                        float x[2];
+#pragma unroll
+                        for (int m = 0; m < 32; ++m) {
+                            const float s = __uint_as_float(m < 16 ? s0[m & 15] : s1[m & 15]);
+                            x[m & 1] = m <= lane ? s * pw[lane - m] : 0.f;
+                            if (m & 1) p[m / 2] = pack_bf16x2(x[0], x[1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int m = 0; m < 16; ++m) p[m] = 0u;
+                }
+                ptx::tmem_st_16(row + 16 * blk, p);
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before_sync();
+            warp_arrive(one(B_PREADY), lane);
+        }
+    }
+
+    // ------------------------------------------------------------ value warps
+    // Thread: one token row of an item, a share of its 16-byte pieces.
+    __device__ void values(int tid, int lane) const {
+        constexpr int PARTS = 128 / Cf::IT, PCS = D / 8 / PARTS;
+        const int r = tid % Cf::IT, part = tid / Cf::IT;
+        const int nc = chunks();
+        for (int c = 0; c < nc; ++c) {
+            const int n = tokens(c);
+            if (!wait(full(tv(c) % Cf::NSLOT), tv(c) / Cf::NSLOT, WD_DC_FULL)) return;
+            uint8_t *v = slot(tv(c));
+            if (n < Cf::C) {
+                // rows past the end multiply zeros: what lies there may be NaN
+                if (!wait(full(tk(c) % Cf::NSLOT), tk(c) / Cf::NSLOT, WD_DC_FULL)) return;
+                if (tid >= n)
+#pragma unroll
+                    for (int j = 0; j < Cf::NAT * (ROWP); ++j) {
+                        const uint32_t off = (j / ROWP) * Cf::SUB + swz_chunk<Cf::AW>(tid, j % ROWP);
+                        *reinterpret_cast<uint4 *>(v + off) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(slot(tk(c)) + off) = make_uint4(0, 0, 0, 0);
+                    }
+            }
+            for (int it = 0; it < Cf::NIT; ++it) {
+                const int i = c * Cf::NIT + it, tok = it * Cf::IT + r;
+                if (i >= Cf::NVB && !wait(vfree(i % Cf::NVB), i / Cf::NVB - 1, WD_DC_VALUE)) return;
+                uint8_t *dst = vbuf(i);
+                const bool live = tok < n;
+                const float w = live ? pw[n - 1 - tok] : 0.f;
+#pragma unroll
+                for (int j = 0; j < PCS; ++j) {
+                    const int pc = part * PCS + j, at = pc / ROWP, cc = pc % ROWP;
+                    uint4 hi = make_uint4(0, 0, 0, 0), mid = hi, lo = hi;
+                    if (live) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(v + at * Cf::SUB + swz_chunk<Cf::AW>(tok, cc));
+                        split(x.x, w, hi.x, mid.x, lo.x);
+                        split(x.y, w, hi.y, mid.y, lo.y);
+                        split(x.z, w, hi.z, mid.z, lo.z);
+                        split(x.w, w, hi.w, mid.w, lo.w);
+                    }
+                    uint8_t *d = dst + at * Cf::VSUB + swz_chunk<Cf::AW>(r, cc);
+                    *reinterpret_cast<uint4 *>(d) = hi;
+                    *reinterpret_cast<uint4 *>(d + Cf::VPART) = mid;
+                    *reinterpret_cast<uint4 *>(d + 2 * Cf::VPART) = lo;
+                }
+                ptx::fence_proxy_async_smem();  // written for the MMA; V read before its slot is filled again
+                warp_arrive(vready(i % Cf::NVB), lane);
+            }
+        }
+    }
+    static constexpr int ROWP = Cf::ROWB / 16;  // 16-byte pieces of a row of one atom
+    // w times a pair of values, as three bf16 parts that add up to the fp32 products
+    __device__ static void split(uint32_t x, float w, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+        float a0 = __uint_as_float(x << 16) * w, a1 = __uint_as_float(x & 0xFFFF0000u) * w;
+        hi = pack_bf16x2(a0, a1);
+        a0 -= __uint_as_float(hi << 16);
+        a1 -= __uint_as_float(hi & 0xFFFF0000u);
+        mid = pack_bf16x2(a0, a1);
+        lo = pack_bf16x2(a0 - __uint_as_float(mid << 16), a1 - __uint_as_float(mid & 0xFFFF0000u));
+    }
+
+    // ------------------------------------------------------------ state and output warps
+    __device__ void states(const DecayMaps &m, int zw, int lane) const {
+        constexpr int NCOL = Cf::NCOL;
+        const int sub = zw & 3, half = zw >> 2, r = 32 * sub + lane, f = r % D;
+        const int col0 = D == 128 ? 64 * half : (r / D) * NCOL;
+        const uint32_t row = tmem + (static_cast<uint32_t>(32 * sub) << 16);
+        float st[NCOL];
+#pragma unroll
+        for (int i = 0; i < NCOL; ++i) st[i] = 0.f;
+        if constexpr (!STATES) {
+            auto add = [&](const float *src, float w) {
+                const float4 *p = reinterpret_cast<const float4 *>(src + (size_t)f * D + col0);
+#pragma unroll
+                for (int i = 0; i < NCOL / 4; ++i) {
+                    const float4 x = p[i];
+                    st[4 * i] = fmaf(w, x.x, st[4 * i]);
+                    st[4 * i + 1] = fmaf(w, x.y, st[4 * i + 1]);
+                    st[4 * i + 2] = fmaf(w, x.z, st[4 * i + 2]);
+                    st[4 * i + 3] = fmaf(w, x.w, st[4 * i + 3]);
+                }
+            };
+            if (a.nseg > 1)
+                for (int s = 0; s <= seg; ++s) add(wsp + (size_t)s * D * D, decay_pow(lg, (float)(begin - s * a.seg)));
+            else if (pool) add(pool, 1.f);
+            put_state(st, f, col0, sbuf(0));
+            warp_arrive(one(B_SREADY), lane);
+        }
+        const DecayMul whole(lg, (float)Cf::C);
+        const float go = a.scale * pw[r + 1];
+        const int nc = chunks();
+        uint8_t *held = nullptr;  // d = 128: the Q slot this warp's last output rows leave from
+        int held_slot = 0;
+        for (int c = 0; c < nc; ++c) {
+            const int n = tokens(c);
+            if (!wait(one(B_KVFULL), c, WD_DC_STATE)) break;
+            ptx::tc_fence_after_sync();
+            const DecayMul mul = n == Cf::C ? whole : DecayMul(lg, (float)n);
+            if constexpr (D == 128) {
+#pragma unroll
+                for (int g = 0; g < 64; g += 32) {
+                    uint32_t x[16], y[16];
+                    ptx::tmem_ld(row + Cf::T_KV + col0 + g, x);
+                    ptx::tmem_ld(row + Cf::T_KV + col0 + g + 16, y);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_pin(x);
+                    ptx::tmem_pin(y);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        st[g + i] = mul(st[g + i]) + __uint_as_float(x[i]);
+                        st[g + 16 + i] = mul(st[g + 16 + i]) + __uint_as_float(y[i]);
+                    }
+                }
+            } else {
+                constexpr int W = NCOL < 16 ? NCOL : 16;
+#pragma unroll
+                for (int g = 0; g < NCOL; g += W) {
+                    uint32_t x[W], y[W];
+                    ptx::tmem_ld(row + Cf::T_KV + col0 + g, x);
+                    ptx::tmem_ld(row + Cf::T_KV + D + col0 + g, y);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_pin(x);
+                    ptx::tmem_pin(y);
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        st[g + i] = mul(st[g + i]) + (__uint_as_float(x[i]) + __uint_as_float(y[i]));
+                }
+            }
+            ptx::tc_fence_before_sync();
+            warp_arrive(one(B_KVEMPTY), lane);
+            if (lane == 0) {
+                ptx::mbar_arrive(empty(tk(c) % Cf::NSLOT));  // K is multiplied (the scores before it, too)
+                if (STATES) ptx::mbar_arrive(empty(tv(c) % Cf::NSLOT));
+            }
+            if constexpr (!STATES) {
+                if (c + 1 < nc) {
+                    // the next chunk's S image: with one buffer, once this chunk's has been multiplied
+                    if (Cf::NSB == 1 && !wait(one(B_QSDONE), c, WD_DC_STATE)) break;
+                    put_state(st, f, col0, sbuf(c + 1));
+                    warp_arrive(one(B_SREADY), lane);
+                }
+                if (held != nullptr) {  // the last chunk's rows have left the Q slot
+                    if (lane == 0) {
+                        ptx::bulk_wait_group_read<0>();
+                        ptx::mbar_arrive(empty(held_slot));
+                    }
+                    held = nullptr;
+                }
+                if (!wait(one(B_OFULL), c, WD_DC_OUT)) break;
+                ptx::tc_fence_after_sync();
+                constexpr int OC = D == 128 ? 64 : D;  // output columns of this thread
+                const int oc0 = D == 128 ? col0 : 0;
+                uint32_t ow[OC / 2];
+#pragma unroll
+                for (int g = 0; g < OC; g += 16) {
+                    uint32_t x[16], y[16];
+                    ptx::tmem_ld(row + Cf::T_OA + oc0 + g, x);
+                    ptx::tmem_ld(row + Cf::T_OI + oc0 + g, y);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_pin(x);
+                    ptx::tmem_pin(y);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2)
+                        ow[(g + i) / 2] = pack_bf16x2(fmaf(go, __uint_as_float(y[i]), a.scale * __uint_as_float(x[i])),
+                                                      fmaf(go, __uint_as_float(y[i + 1]), a.scale * __uint_as_float(x[i + 1])));
+                }
+                ptx::tc_fence_before_sync();
+                warp_arrive(one(B_OEMPTY), lane);
+                if (lane == 0) {
+                    ptx::mbar_arrive(empty(tv(c) % Cf::NSLOT));
+                    if (D != 128) {
+                        ptx::mbar_arrive(empty(tq(c) % Cf::NSLOT));
+                        ptx::bulk_wait_group_read<0>();  // the staged rows of the last chunk have left
+                    }
+                }
+                __syncwarp();
+                uint8_t *stg = D == 128 ? slot(tq(c)) + half * Cf::SUB + 32 * sub * Cf::ROWB
+                                        : base + Cf::OFF_O + 32 * sub * Cf::ROWB;
+#pragma unroll
+                for (int j = 0; j < OC / 8; ++j) {
+                    uint4 x = make_uint4(ow[4 * j], ow[4 * j + 1], ow[4 * j + 2], ow[4 * j + 3]);
+                    if (r >= n) x = make_uint4(0, 0, 0, 0);  // rows past the prompt's end are zeros
+                    *reinterpret_cast<uint4 *>(stg + swz_chunk<Cf::AW>(lane, j)) = x;
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    const MapCoord mc = map_coord(begin + c * Cf::C + 32 * sub, h, m.swap_o);
+                    if (begin + c * Cf::C + 32 * sub < a.N)
+                        ptx::tma_store_4d_hint(&m.o, ptx::smem_u32(stg), oc0, mc.y, mc.z, b, ptx::l2_evict_first());
+                    ptx::bulk_commit_group();
+                }
+                if (D == 128) {
+                    held = stg;
+                    held_slot = tq(c) % Cf::NSLOT;
+                }
+            }
+        }
+        if constexpr (STATES) {
+            store_state(st, wsp + (size_t)(seg + 1) * D * D, f, col0);
+        } else {
+            if (pool && end > begin && !more()) store_state(st, pool, f, col0);
+            if (lane == 0) ptx::bulk_wait_group_read<0>();  // staged rows have left before the CTA's memory goes
+        }
+    }
+    // whether the prompt goes on behind this segment
+    __device__ bool more() const { return end < decay_len(a, b); }
+    __device__ static void store_state(const float (&st)[Cf::NCOL], float *dst, int f, int col0) {
+        float4 *p = reinterpret_cast<float4 *>(dst + (size_t)f * D + col0);
+#pragma unroll
+        for (int i = 0; i < Cf::NCOL / 4; ++i) p[i] = make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
+    }
+    // this thread's part of the state as a bf16 operand image
+    __device__ static void put_state(const float (&st)[Cf::NCOL], int f, int col0, uint8_t *img) {
+#pragma unroll
+        for (int j = 0; j < Cf::NCOL / 8; ++j) {
+            const int pc = col0 / 8 + j;
+            const float *s = st + 8 * j;
+            *reinterpret_cast<uint4 *>(img + (pc / ROWP) * D * Cf::ROWB + swz_chunk<Cf::AW>(f, pc % ROWP)) = make_uint4(
+                pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+        }
+        ptx::fence_proxy_async_smem();
+    }
+};
+
+template <int D, bool STATES>
+__global__ void __launch_bounds__(DecayTc<D, STATES>::THREADS, D == 32 ? 2 : 1)
+    decay_tc_kernel(const __grid_constant__ DecayMaps m, const __grid_constant__ DecayArgs a) {
+    using Cf = DecayTc<D, STATES>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = align1024(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = STATES ? a.nseg - 1 : a.nseg;
+    const int bh = blockIdx.x / per, seg = blockIdx.x - bh * per;
+    const int b = bh / a.H, h = bh - b * a.H;
+    const int slot = decay_slot(a, b);
+    const int L = slot < 0 ? 0 : decay_len(a, b);
+    const int begin = seg * a.seg, stop = min(begin + a.seg, a.N);
+    float *pool = a.S && slot >= 0 ? a.S + ((size_t)slot * a.H + h) * D * D : nullptr;
+    float *wsp = a.ws + (size_t)bh * a.nseg * D * D;
+    if (STATES && seg == 0)  // the second launch may overwrite the pool while others still read the entering state
+        for (int i = tid; i < D * D / 4; i += Cf::THREADS)
+            reinterpret_cast<float4 *>(wsp)[i] =
+                pool ? reinterpret_cast<const float4 *>(pool)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+    const int end = min(stop, L);
+    if (end > begin) {
+        const float lg = decay_log(a.log_decay, h);
+        uint64_t *bars = reinterpret_cast<uint64_t *>(base + Cf::OFF_CTRL);
+        volatile int *flag = reinterpret_cast<volatile int *>(base + Cf::OFF_CTRL + 248);
+        uint32_t *tslot = reinterpret_cast<uint32_t *>(base + Cf::OFF_CTRL + 252);
+        float *pw = reinterpret_cast<float *>(base + Cf::OFF_PW);
+        DecayUnit<D, STATES> u{a, base, bars, flag, pw, pw + 132, 0u, b, h, begin, end, lg, pool, wsp, seg};
+        if (tid == 0) {
+            *flag = 0;
+            u.init_barriers();
+            ptx::fence_mbar_init();
+        }
+        if (tid < 129) pw[tid] = decay_pow(lg, (float)tid);
+        else if (tid < 161) pw[132 + tid - 129] = decay_pow(lg, (float)(31 - (tid - 129)));
+        if (warp == 0) {
+            ptx::tmem_alloc(ptx::smem_u32(tslot), Cf::TCOLS);
+            ptx::tmem_relinquish();
+        }
+        ptx::tc_fence_before_sync();
+        __syncthreads();
+        ptx::tc_fence_after_sync();
+        u.tmem = *tslot;
+        constexpr int X = Cf::XW, T = X + Cf::TW, U = T + Cf::UW;
+        if (warp < X) {
+            u.scores(warp, lane);
+        } else if (warp < T) {
+            u.values(tid - 32 * X, lane);
+        } else if (warp < U) {
+            u.states(m, warp - T, lane);
+        } else if (lane == 0) {
+            if (warp == U) u.producer(m);
+            else u.mma();
+        }
+        ptx::tc_fence_before_sync();
+        __syncthreads();
+        if (warp == 0) {
+            ptx::tc_fence_after_sync();
+            ptx::tmem_dealloc(u.tmem, Cf::TCOLS);
+        }
+    } else if (STATES) {
+        float4 *dst = reinterpret_cast<float4 *>(wsp + (size_t)(seg + 1) * D * D);
+        for (int i = tid; i < D * D / 4; i += Cf::THREADS) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (!STATES) {
+        // rows behind the last chunk (whose own rows past the end went out as zeros)
+        const int z0 = max(begin, begin + (max(end - begin, 0) + Cf::C - 1) / Cf::C * Cf::C);
+        __nv_bfloat16 *op = static_cast<__nv_bfloat16 *>(a.o) + b * a.lo.batch + h * a.lo.head;
+        for (long long i = tid; i < (long long)(stop - z0) * (D / 8); i += Cf::THREADS)
+            *reinterpret_cast<uint4 *>(op + (z0 + i / (D / 8)) * a.lo.tok + i % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+    }
+}
+
+}  // namespace blin
