@@ -68,6 +68,17 @@ struct DecayMul {
     __device__ __forceinline__ float operator()(float s) const { return near ? fmaf(s, m, s) : s * m; }
 };
 
+// g^n as the sum of an fp32 value and the rest, so that a state multiplied by it at
+// every chunk does not collect the same rounding error of g^n each time.
+struct DecaySplit {
+    float hi, lo;
+    __device__ __forceinline__ DecaySplit(float lg, float n) {
+        const DecayMul m(lg, n);
+        hi = m.near ? 1.f + m.m : m.m;
+        lo = m.near ? (1.f - hi) + m.m : 0.f;
+    }
+};
+
 // The pool slot of batch row b, -1 when the row is idle (all threads of the
 // block call it).  An entry out of range, or one that an earlier row has, makes
 // the row idle and is recorded in the watchdog word.

@@ -46,18 +46,20 @@ struct DecayTc {
     static constexpr int OSTG = STATES || D == 128 ? 0 : TILE;      // output staging (d = 128: in the chunk's Q slot)
     static constexpr int OFF_V = NSLOT * TILE, OFF_S = OFF_V + NVB * VITEM, OFF_O = OFF_S + (STATES ? 0 : NSB * SIMG);
     static constexpr int OFF_CTRL = OFF_O + OSTG;
-    static constexpr int NBAR = 2 * NSLOT + 2 * NVB + 9;
-    static constexpr int OFF_PW = OFF_CTRL + 256;  // g^n for n = 0 .. 128, then g^{31 - m} for m < 32
+    static constexpr int NBAR = 2 * NSLOT + 2 * NVB + 11;
+    static constexpr int OFF_PW = OFF_CTRL + 512;  // g^n for n = 0 .. 128, then scale g^{31 - m} for m < 32
     static constexpr int BYTES = OFF_PW + 4 * (132 + 32) + 1024;
-    static_assert(8 * NBAR <= 248, "barriers");
+    static_assert(8 * NBAR <= 504, "barriers");
     static_assert(BYTES <= 227 * 1024, "shared memory");
     // warps
     static constexpr int XW = STATES ? 0 : 4, TW = 4, UW = D == 128 ? 8 : 4;
-    static constexpr int THREADS = 32 * (XW + TW + UW + 2);
-    // TMEM columns: scores / P, inner and carried outputs, state product (high part | rest, or all of it)
-    static constexpr int KVC = D == 128 ? 128 : 2 * D;
+    static constexpr int THREADS = 32 * (XW + TW + UW + (STATES ? 2 : 3));
+    // TMEM columns: scores / P, inner and carried outputs, state product.  The three parts of the values
+    // multiply side by side where there is room for a column range each (KVN = 3), else the low part is
+    // added to the middle one's (2), or all to one (1).
+    static constexpr int KVN = D == 128 ? 1 : D == 64 || STATES ? 3 : 2, KVC = KVN * D;
     static constexpr int T_OA = 128, T_OI = T_OA + D, T_KV = STATES ? 0 : T_OI + D;
-    static constexpr int TCOLS = STATES ? KVC : D == 32 ? 256 : 512;
+    static constexpr int TCOLS = STATES ? (D == 64 ? 256 : 128) : D == 32 ? 256 : 512;
     static_assert(T_KV + KVC <= TCOLS, "TMEM columns");
     static constexpr int NCOL = D == 128 ? 64 : D * D / 128;  // state columns per thread
 };
@@ -74,7 +76,6 @@ struct DecayUnit {
     const DecayArgs &a;
     uint8_t *base;
     uint64_t *bars;
-    volatile int *flag;
     float *pw, *lead;
     uint32_t tmem;
     int b, h, begin, end;  // tokens [begin, end) of batch row b, head h
@@ -82,8 +83,15 @@ struct DecayUnit {
     float *pool, *wsp;
     int seg;
 
-    // barriers: full/empty of the landing slots, ready/free of the weighted values, then one each
-    enum { B_SFULL, B_PREADY, B_KVFULL, B_KVEMPTY, B_SREADY, B_QSDONE, B_OFULL, B_OEMPTY, B_DRAIN };
+    // Barriers: full/empty of the landing slots, ready/free of the weighted values, then one each.  A wait
+    // names a completion by its parity, so none may run two completions ahead of a role that waits for it:
+    //   B_SREADY   two barriers in turn: the states' chain may finish chunk c's product, and the image of
+    //              chunk c + 1 with it, before the outputs' thread asks for chunk c's image, but no further
+    //              (the next image waits for chunk c's outputs);
+    //   B_CLEAN    completes once, in a last chunk with rows past the prompt's end;
+    //   all others are completed again only after what waits for them has passed.
+    enum { B_SFULL, B_PREADY, B_KVFULL, B_KVEMPTY, B_SREADY, B_SREADY1, B_QSDONE, B_OFULL, B_OEMPTY, B_CLEAN, B_DRAIN };
+    __device__ uint32_t sready(int c) const { return one(B_SREADY + (c & 1)); }
     __device__ uint32_t bar(int i) const { return ptx::smem_u32(bars + i); }
     __device__ uint32_t full(int s) const { return bar(s); }
     __device__ uint32_t empty(int s) const { return bar(Cf::NSLOT + s); }
@@ -112,17 +120,16 @@ struct DecayUnit {
         ptx::mbar_init(one(B_KVFULL), 1);
         ptx::mbar_init(one(B_KVEMPTY), Cf::UW);
         ptx::mbar_init(one(B_SREADY), Cf::UW);
+        ptx::mbar_init(one(B_SREADY1), Cf::UW);
+        ptx::mbar_init(one(B_CLEAN), Cf::TW);
         ptx::mbar_init(one(B_QSDONE), 1);
         ptx::mbar_init(one(B_OFULL), 1);
         ptx::mbar_init(one(B_OEMPTY), Cf::UW);
-        ptx::mbar_init(one(B_DRAIN), 1);
+        ptx::mbar_init(one(B_DRAIN), STATES ? 1 : 2);
     }
-    // Waits for the phase's completion number `k` (from 0); false: gave up, or another role has.
-    __device__ bool wait(uint32_t br, int k, int code) const {
-        if (ptx::mbar_wait_bounded(br, k & 1, a.wd, code, kWaitLimitNs) && !*flag) return true;
-        *flag = 1;
-        return false;
-    }
+    // Waits for completion number `k` (from 0) of a barrier; false: gave up.  A role that gives up stops,
+    // and those that wait for it give up in turn.
+    __device__ bool wait(uint32_t br, int k, int code) const { return mbar_wait_patient(br, k & 1, a.wd, code); }
     __device__ int chunks() const { return (end - begin + Cf::C - 1) / Cf::C; }
     __device__ int tokens(int c) const { return min(Cf::C, end - begin - c * Cf::C); }
 
@@ -152,136 +159,149 @@ struct DecayUnit {
             ptx::mbar_wait_bounded(full(u % Cf::NSLOT), (u / Cf::NSLOT) & 1, a.wd, WD_DC_FULL, kWaitLimitNs);
     }
 
-    // ------------------------------------------------------------ MMA issuer (one thread)
-    __device__ void mma() const {
-        constexpr int ROWB = Cf::ROWB, KT = 8 * ROWB;  // bytes of 8 rows
+    // ------------------------------------------------------------ MMA issuers (one thread each)
+    // An operand's descriptor is a constant plus its address in 16-byte units.
+    __device__ static uint64_t kmajor(uint32_t addr) { return ptx::smem_desc(addr, 16, 8 * Cf::ROWB, Cf::LAYOUT); }
+    __device__ static uint64_t mnmajor(uint32_t addr, uint32_t atom) {
+        return ptx::smem_desc(addr, atom, 8 * Cf::ROWB, Cf::LAYOUT);
+    }
+    // 16 features further along a K-major tile
+    __device__ static uint64_t kstep(int kk) {
+        return static_cast<uint64_t>((kk / (Cf::AW / 16)) * (Cf::SUB / 16) + (kk % (Cf::AW / 16)) * 2);
+    }
+    // scores and outputs
+    __device__ void mma_outputs() const {
+        const int nc = chunks();
+        for (int c = 0; c < nc; ++c) {
+            if (!wait(full(tk(c) % Cf::NSLOT), tk(c) / Cf::NSLOT, WD_DC_FULL) ||
+                !wait(full(tq(c) % Cf::NSLOT), tq(c) / Cf::NSLOT, WD_DC_FULL))
+                break;
+            // a chunk with rows past the prompt's end: once those are cleared
+            if (tokens(c) < Cf::C && !wait(one(B_CLEAN), 0, WD_DC_VALUE)) break;
+            const uint64_t qd = kmajor(ptx::smem_u32(slot(tq(c)))), kd = kmajor(ptx::smem_u32(slot(tk(c))));
+            // the scores' columns were last read by the PV product that this thread issued before
+            constexpr uint32_t IDS = ptx::idesc_bf16_f32(128, 128, 0, 0), IDO = ptx::idesc_bf16_f32(128, D, 0, 1);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) ptx::mma_bf16_ss(tmem, qd + kstep(kk), kd + kstep(kk), IDS, kk > 0);
+            ptx::mma_commit(one(B_SFULL));
+            if (!wait(sready(c), c >> 1, WD_DC_STATE) || (c > 0 && !wait(one(B_OEMPTY), c - 1, WD_DC_OUT))) break;
+            ptx::tc_fence_after_sync();
+            const uint64_t sd = mnmajor(ptx::smem_u32(sbuf(c)), D * Cf::ROWB);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                ptx::mma_bf16_ss(tmem + Cf::T_OI, qd + kstep(kk), sd + static_cast<uint64_t>(kk * Cf::ROWB), IDO, kk > 0);
+            if (Cf::NSB == 1) ptx::mma_commit(one(B_QSDONE));
+            if (!wait(full(tv(c) % Cf::NSLOT), tv(c) / Cf::NSLOT, WD_DC_FULL) || !wait(one(B_PREADY), c, WD_DC_SCORE)) break;
+            ptx::tc_fence_after_sync();
+            const uint64_t vd = mnmajor(ptx::smem_u32(slot(tv(c))), Cf::SUB);
+#pragma unroll
+            for (int kk = 0; kk < Cf::C / 16; ++kk)
+                ptx::mma_bf16_ts(tmem + Cf::T_OA, tmem + 8 * kk, vd + static_cast<uint64_t>(kk * Cf::ROWB), IDO, kk > 0);
+            ptx::mma_commit(one(B_OFULL));
+        }
+        drain();
+    }
+    // state product, item by item
+    __device__ void mma_states() const {
         const int nc = chunks();
         for (int c = 0; c < nc; ++c) {
             if (!wait(full(tk(c) % Cf::NSLOT), tk(c) / Cf::NSLOT, WD_DC_FULL)) break;
-            const uint32_t ka = ptx::smem_u32(slot(tk(c)));
-            uint32_t qa = 0;
-            if constexpr (!STATES) {
-                if (!wait(full(tq(c) % Cf::NSLOT), tq(c) / Cf::NSLOT, WD_DC_FULL)) break;
-                qa = ptx::smem_u32(slot(tq(c)));
-                // the scores' columns were last read by the PV product issued before this one
-                constexpr uint32_t ID = ptx::idesc_bf16_f32(128, 128, 0, 0);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const int at = kk / (Cf::AW / 16), jj = kk % (Cf::AW / 16);
-                    ptx::mma_bf16_ss(tmem, ptx::smem_desc(qa + at * Cf::SUB + 32 * jj, 16, KT, Cf::LAYOUT),
-                                     ptx::smem_desc(ka + at * Cf::SUB + 32 * jj, 16, KT, Cf::LAYOUT), ID, kk > 0);
-                }
-                ptx::mma_commit(one(B_SFULL));
-            }
-            // state product, item by item
             if (c > 0 && !wait(one(B_KVEMPTY), c - 1, WD_DC_STATE)) break;
+            const uint64_t kd = mnmajor(ptx::smem_u32(slot(tk(c))), D == 128 ? Cf::SUB : 0);
             bool ok = true;
+#pragma unroll 1
             for (int it = 0; it < Cf::NIT; ++it) {
                 const int i = c * Cf::NIT + it;
                 if (!(ok = wait(vready(i % Cf::NVB), i / Cf::NVB, WD_DC_VALUE))) break;
                 ptx::tc_fence_after_sync();
-                const uint64_t ad = ptx::smem_desc(ka, D == 128 ? Cf::SUB : 0, KT, Cf::LAYOUT) + it * (Cf::IT / 16) * ROWB;
-                const uint32_t vb = ptx::smem_u32(vbuf(i));
+                const uint64_t ad = kd + static_cast<uint64_t>(it * (Cf::IT / 16) * Cf::ROWB);
+                const uint64_t vd = mnmajor(ptx::smem_u32(vbuf(i)), Cf::VSUB);
 #pragma unroll
                 for (int kk = 0; kk < Cf::IT / 16; ++kk) {
-                    const uint64_t bo = static_cast<uint64_t>(kk * ROWB);
+                    const uint64_t bo = static_cast<uint64_t>(kk * Cf::ROWB);
                     const uint32_t acc = it > 0 || kk > 0;
-                    if constexpr (D == 128) {  // small parts first
-                        constexpr uint32_t ID = ptx::idesc_bf16_f32(128, 128, 1, 1);
+                    constexpr uint32_t ID = ptx::idesc_bf16_f32(128, Cf::KVN * D, 1, 1), ID1 = ptx::idesc_bf16_f32(128, D, 1, 1);
+                    if constexpr (Cf::KVN == 1) {  // small parts first
 #pragma unroll
                         for (int part = 2; part >= 0; --part)
-                            ptx::mma_bf16_ss(tmem + Cf::T_KV, ad + bo,
-                                             ptx::smem_desc(vb + part * Cf::VPART, Cf::VSUB, KT, Cf::LAYOUT) + bo, ID,
-                                             acc | (part < 2));
+                            ptx::mma_bf16_ss(tmem + Cf::T_KV, ad + bo, vd + part * (Cf::VPART / 16) + bo, ID1, acc | (part < 2));
                     } else {
-                        // the low part into the middle part's columns, then high | middle
-                        constexpr uint32_t IDL = ptx::idesc_bf16_f32(128, D, 1, 1), IDH = ptx::idesc_bf16_f32(128, 2 * D, 1, 1);
-                        ptx::mma_bf16_ss(tmem + Cf::T_KV, ad + bo, ptx::smem_desc(vb, Cf::VSUB, KT, Cf::LAYOUT) + bo, IDH, acc);
-                        ptx::mma_bf16_ss(tmem + Cf::T_KV + D, ad + bo,
-                                         ptx::smem_desc(vb + 2 * Cf::VPART, Cf::VSUB, KT, Cf::LAYOUT) + bo, IDL, 1u);
+                        ptx::mma_bf16_ss(tmem + Cf::T_KV, ad + bo, vd + bo, ID, acc);
+                        if constexpr (Cf::KVN == 2)
+                            ptx::mma_bf16_ss(tmem + Cf::T_KV + D, ad + bo, vd + 2 * (Cf::VPART / 16) + bo, ID1, 1u);
                     }
                 }
                 ptx::mma_commit(vfree(i % Cf::NVB));
             }
             if (!ok) break;
             ptx::mma_commit(one(B_KVFULL));
-            if constexpr (!STATES) {
-                if (!wait(one(B_SREADY), c, WD_DC_STATE)) break;
-                if (c > 0 && !wait(one(B_OEMPTY), c - 1, WD_DC_OUT)) break;
-                if (!wait(full(tv(c) % Cf::NSLOT), tv(c) / Cf::NSLOT, WD_DC_FULL)) break;
-                ptx::tc_fence_after_sync();
-                constexpr uint32_t ID = ptx::idesc_bf16_f32(128, D, 0, 1);
-                const uint64_t sd = ptx::smem_desc(ptx::smem_u32(sbuf(c)), D * ROWB, KT, Cf::LAYOUT);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const int at = kk / (Cf::AW / 16), jj = kk % (Cf::AW / 16);
-                    ptx::mma_bf16_ss(tmem + Cf::T_OI, ptx::smem_desc(qa + at * Cf::SUB + 32 * jj, 16, KT, Cf::LAYOUT),
-                                     sd + static_cast<uint64_t>(kk * ROWB), ID, kk > 0);
-                }
-                if (Cf::NSB == 1) ptx::mma_commit(one(B_QSDONE));
-                if (!wait(one(B_PREADY), c, WD_DC_SCORE)) break;
-                ptx::tc_fence_after_sync();
-                const uint64_t vd = ptx::smem_desc(ptx::smem_u32(slot(tv(c))), Cf::SUB, KT, Cf::LAYOUT);
-#pragma unroll
-                for (int kk = 0; kk < Cf::C / 16; ++kk)
-                    ptx::mma_bf16_ts(tmem + Cf::T_OA, tmem + 8 * kk, vd + static_cast<uint64_t>(kk * ROWB), ID, kk > 0);
-                ptx::mma_commit(one(B_OFULL));
-            }
         }
-        // every MMA and the arrivals of its commit complete before TMEM is released
+        drain();
+    }
+    // every MMA, and the arrivals of its commit, completes before TMEM is released
+    __device__ void drain() const {
         ptx::mma_commit(one(B_DRAIN));
-        ptx::mbar_wait_bounded(one(B_DRAIN), 0, a.wd, WD_DC_DRAIN, kWaitLimitNs);
+        wait(one(B_DRAIN), 0, WD_DC_DRAIN);
     }
 
     // ------------------------------------------------------------ score warps (row i per thread)
+    // The weights scale g^{i-j} of the diagonal block stay in registers (0 right of the diagonal); left of
+    // it they are g^{i - 32 blk - 31} * scale g^{31 - (j - 32 blk)}, both powers >= 0.
     __device__ void scores(int w, int lane) const {
         const uint32_t row = tmem + (static_cast<uint32_t>(32 * w) << 16);
-        // g^{i-j} = g^{i - 32 blk - 31} * g^{31 - (j - 32 blk)} left of the diagonal block: both powers >= 0
-        float far[3];
+        float dw[32];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) far[k] = pw[32 * k + 1 + lane];
+        for (int m = 0; m < 32; ++m) dw[m] = m <= lane ? a.scale * pw[lane - m] : 0.f;
         const int nc = chunks();
         for (int c = 0; c < nc; ++c) {
             if (!wait(one(B_SFULL), c, WD_DC_SCORE)) break;
             ptx::tc_fence_after_sync();
+#pragma unroll 1
+            for (int g = 0; g < 2 * w; ++g) {  // 16 columns at a time
+                uint32_t s[16], p[8];
+                ptx::tmem_ld(row + 16 * g, s);
+                const float f = pw[32 * (w - (g >> 1) - 1) + 1 + lane];
+                const float4 *l4 = reinterpret_cast<const float4 *>(lead + 16 * (g & 1));
+                ptx::tmem_wait_ld();
+                ptx::tmem_pin(s);
 #pragma unroll
-            for (int blk = 0; blk < 4; ++blk) {
-                uint32_t p[16];
-                if (blk <= w) {
-                    uint32_t s0[16], s1[16];
-                    ptx::tmem_ld(row + 32 * blk, s0);
-                    ptx::tmem_ld(row + 32 * blk + 16, s1);
-                    ptx::tmem_wait_ld();
-                    ptx::tmem_pin(s0);
-                    ptx::tmem_pin(s1);
-                    if (blk < w) {
-                        const float f = w - blk == 1 ? far[0] : w - blk == 2 ? far[1] : far[2];
-#pragma unroll
-                        for (int m = 0; m < 32; m += 4) {
-                            const float4 l = *reinterpret_cast<const float4 *>(lead + m);
-                            auto s = [&](int x) { return __uint_as_float(x < 16 ? s0[x & 15] : s1[x & 15]); };
-                            p[m / 2] = pack_bf16x2(s(m) * (f * l.x), s(m + 1) * (f * l.y));
-                            p[m / 2 + 1] = pack_bf16x2(s(m + 2) * (f * l.z), s(m + 3) * (f * l.w));
-                        }
-                    } else {
-                        float x[2];
-#pragma unroll
-                        for (int m = 0; m < 32; ++m) {
-                            const float s = __uint_as_float(m < 16 ? s0[m & 15] : s1[m & 15]);
-                            x[m & 1] = m <= lane ? s * pw[lane - m] : 0.f;
-                            if (m & 1) p[m / 2] = pack_bf16x2(x[0], x[1]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int m = 0; m < 16; ++m) p[m] = 0u;
+                for (int m = 0; m < 16; m += 4) {
+                    const float4 l = l4[m / 4];
+                    const float2 x = mul2(s[m], s[m + 1], mul2(f, f, l.x, l.y)), y = mul2(s[m + 2], s[m + 3], mul2(f, f, l.z, l.w));
+                    p[m / 2] = pack_bf16x2(x.x, x.y);
+                    p[m / 2 + 1] = pack_bf16x2(y.x, y.y);
                 }
-                ptx::tmem_st_16(row + 16 * blk, p);
+                ptx::tmem_st(row + 8 * g, p);
             }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                uint32_t s[16], p[8];
+                ptx::tmem_ld(row + 32 * w + 16 * g, s);
+                ptx::tmem_wait_ld();
+                ptx::tmem_pin(s);
+#pragma unroll
+                for (int m = 0; m < 16; m += 2) {
+                    const float2 x = mul2(s[m], s[m + 1], make_float2(dw[16 * g + m], dw[16 * g + m + 1]));
+                    p[m / 2] = pack_bf16x2(x.x, x.y);
+                }
+                ptx::tmem_st(row + 16 * w + 8 * g, p);
+            }
+            const uint32_t zero[8] = {};
+#pragma unroll 1
+            for (int g = 2 * w + 2; g < 8; ++g) ptx::tmem_st(row + 8 * g, zero);
             ptx::tmem_wait_st();
             ptx::tc_fence_before_sync();
             warp_arrive(one(B_PREADY), lane);
         }
+    }
+    __device__ static float2 mul2(float x, float y, float u, float v) { return mul2(__float_as_uint(x), __float_as_uint(y), make_float2(u, v)); }
+    // two products in one instruction
+    __device__ static float2 mul2(uint32_t x, uint32_t y, float2 b) {
+        float2 r;
+        asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n}\n"
+            : "=f"(r.x), "=f"(r.y)
+            : "r"(x), "r"(y), "f"(b.x), "f"(b.y));
+        return r;
     }
 
     // ------------------------------------------------------------ value warps
@@ -304,14 +324,17 @@ struct DecayUnit {
                         *reinterpret_cast<uint4 *>(v + off) = make_uint4(0, 0, 0, 0);
                         *reinterpret_cast<uint4 *>(slot(tk(c)) + off) = make_uint4(0, 0, 0, 0);
                     }
+                ptx::fence_proxy_async_smem();
+                warp_arrive(one(B_CLEAN), lane);
             }
+#pragma unroll 1
             for (int it = 0; it < Cf::NIT; ++it) {
                 const int i = c * Cf::NIT + it, tok = it * Cf::IT + r;
                 if (i >= Cf::NVB && !wait(vfree(i % Cf::NVB), i / Cf::NVB - 1, WD_DC_VALUE)) return;
                 uint8_t *dst = vbuf(i);
                 const bool live = tok < n;
                 const float w = live ? pw[n - 1 - tok] : 0.f;
-#pragma unroll
+#pragma unroll 2
                 for (int j = 0; j < PCS; ++j) {
                     const int pc = part * PCS + j, at = pc / ROWP, cc = pc % ROWP;
                     uint4 hi = make_uint4(0, 0, 0, 0), mid = hi, lo = hi;
@@ -333,14 +356,19 @@ struct DecayUnit {
         }
     }
     static constexpr int ROWP = Cf::ROWB / 16;  // 16-byte pieces of a row of one atom
-    // w times a pair of values, as three bf16 parts that add up to the fp32 products
+    // w times a pair of values, as three bf16 parts that add up to the fp32 products: the upper 16 bits, the
+    // upper 16 bits of what is left (exact differences), and the rest, at most 8 significant bits
     __device__ static void split(uint32_t x, float w, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-        float a0 = __uint_as_float(x << 16) * w, a1 = __uint_as_float(x & 0xFFFF0000u) * w;
-        hi = pack_bf16x2(a0, a1);
-        a0 -= __uint_as_float(hi << 16);
-        a1 -= __uint_as_float(hi & 0xFFFF0000u);
-        mid = pack_bf16x2(a0, a1);
-        lo = pack_bf16x2(a0 - __uint_as_float(mid << 16), a1 - __uint_as_float(mid & 0xFFFF0000u));
+        float2 v = mul2(x << 16, x & 0xFFFF0000u, make_float2(w, w));
+        hi = upper(v);
+        v = rest(v);
+        mid = upper(v);
+        lo = upper(rest(v));
+    }
+    __device__ static uint32_t upper(float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); }
+    __device__ static float2 rest(float2 v) {
+        return make_float2(v.x - __uint_as_float(__float_as_uint(v.x) & 0xFFFF0000u),
+                           v.y - __uint_as_float(__float_as_uint(v.y) & 0xFFFF0000u));
     }
 
     // ------------------------------------------------------------ state and output warps
@@ -368,116 +396,90 @@ struct DecayUnit {
                 for (int s = 0; s <= seg; ++s) add(wsp + (size_t)s * D * D, decay_pow(lg, (float)(begin - s * a.seg)));
             else if (pool) add(pool, 1.f);
             put_state(st, f, col0, sbuf(0));
-            warp_arrive(one(B_SREADY), lane);
+            warp_arrive(sready(0), lane);
         }
-        const DecayMul whole(lg, (float)Cf::C);
+        const DecaySplit whole(lg, (float)Cf::C);
         const float go = a.scale * pw[r + 1];
         const int nc = chunks();
-        uint8_t *held = nullptr;  // d = 128: the Q slot this warp's last output rows leave from
-        int held_slot = 0;
+        int held = -1;  // d = 128: the Q slot this warp's last output rows leave from
         for (int c = 0; c < nc; ++c) {
             const int n = tokens(c);
             if (!wait(one(B_KVFULL), c, WD_DC_STATE)) break;
             ptx::tc_fence_after_sync();
-            const DecayMul mul = n == Cf::C ? whole : DecayMul(lg, (float)n);
-            if constexpr (D == 128) {
+            DecaySplit g = whole;
+            if (n < Cf::C) g = DecaySplit(lg, (float)n);
+            constexpr int W = 8;
 #pragma unroll
-                for (int g = 0; g < 64; g += 32) {
-                    uint32_t x[16], y[16];
-                    ptx::tmem_ld(row + Cf::T_KV + col0 + g, x);
-                    ptx::tmem_ld(row + Cf::T_KV + col0 + g + 16, y);
-                    ptx::tmem_wait_ld();
-                    ptx::tmem_pin(x);
-                    ptx::tmem_pin(y);
+            for (int i0 = 0; i0 < NCOL; i0 += W) {
+                uint32_t x[Cf::KVN][W];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        st[g + i] = mul(st[g + i]) + __uint_as_float(x[i]);
-                        st[g + 16 + i] = mul(st[g + 16 + i]) + __uint_as_float(y[i]);
-                    }
-                }
-            } else {
-                constexpr int W = NCOL < 16 ? NCOL : 16;
+                for (int p = 0; p < Cf::KVN; ++p) ptx::tmem_ld(row + Cf::T_KV + p * D + col0 + i0, x[p]);
+                ptx::tmem_wait_ld();
 #pragma unroll
-                for (int g = 0; g < NCOL; g += W) {
-                    uint32_t x[W], y[W];
-                    ptx::tmem_ld(row + Cf::T_KV + col0 + g, x);
-                    ptx::tmem_ld(row + Cf::T_KV + D + col0 + g, y);
-                    ptx::tmem_wait_ld();
-                    ptx::tmem_pin(x);
-                    ptx::tmem_pin(y);
+                for (int p = 0; p < Cf::KVN; ++p) ptx::tmem_pin(x[p]);
 #pragma unroll
-                    for (int i = 0; i < W; ++i)
-                        st[g + i] = mul(st[g + i]) + (__uint_as_float(x[i]) + __uint_as_float(y[i]));
+                for (int i = 0; i < W; ++i) {
+                    float t = __uint_as_float(x[Cf::KVN - 1][i]);
+#pragma unroll
+                    for (int p = Cf::KVN - 2; p >= 0; --p) t += __uint_as_float(x[p][i]);
+                    st[i0 + i] = fmaf(st[i0 + i], g.hi, fmaf(st[i0 + i], g.lo, t));
                 }
             }
             ptx::tc_fence_before_sync();
             warp_arrive(one(B_KVEMPTY), lane);
-            if (lane == 0) {
-                ptx::mbar_arrive(empty(tk(c) % Cf::NSLOT));  // K is multiplied (the scores before it, too)
-                if (STATES) ptx::mbar_arrive(empty(tv(c) % Cf::NSLOT));
-            }
-            if constexpr (!STATES) {
+            if constexpr (STATES) {
+                if (lane == 0) {
+                    ptx::mbar_arrive(empty(tk(c) % Cf::NSLOT));
+                    ptx::mbar_arrive(empty(tv(c) % Cf::NSLOT));
+                }
+            } else {
                 if (c + 1 < nc) {
                     // the next chunk's S image: with one buffer, once this chunk's has been multiplied
                     if (Cf::NSB == 1 && !wait(one(B_QSDONE), c, WD_DC_STATE)) break;
                     put_state(st, f, col0, sbuf(c + 1));
-                    warp_arrive(one(B_SREADY), lane);
+                    warp_arrive(sready(c + 1), lane);
                 }
-                if (held != nullptr) {  // the last chunk's rows have left the Q slot
-                    if (lane == 0) {
-                        ptx::bulk_wait_group_read<0>();
-                        ptx::mbar_arrive(empty(held_slot));
-                    }
-                    held = nullptr;
+                if (lane == 0 && c > 0) {  // the staged rows of the last chunk have left
+                    ptx::bulk_wait_group_read<0>();
+                    if (D == 128) ptx::mbar_arrive(empty(held));
                 }
+                __syncwarp();
                 if (!wait(one(B_OFULL), c, WD_DC_OUT)) break;
                 ptx::tc_fence_after_sync();
                 constexpr int OC = D == 128 ? 64 : D;  // output columns of this thread
                 const int oc0 = D == 128 ? col0 : 0;
-                uint32_t ow[OC / 2];
-#pragma unroll
-                for (int g = 0; g < OC; g += 16) {
-                    uint32_t x[16], y[16];
-                    ptx::tmem_ld(row + Cf::T_OA + oc0 + g, x);
-                    ptx::tmem_ld(row + Cf::T_OI + oc0 + g, y);
+                uint8_t *stg = D == 128 ? slot(tq(c)) + half * Cf::SUB + 32 * sub * Cf::ROWB
+                                        : base + Cf::OFF_O + 32 * sub * Cf::ROWB;
+                const uint32_t keep = r < n ? ~0u : 0u;  // rows past the prompt's end are zeros
+#pragma unroll 1
+                for (int j = 0; j < OC / 8; ++j) {
+                    uint32_t x[8], y[8], o[4];
+                    ptx::tmem_ld(row + Cf::T_OA + oc0 + 8 * j, x);
+                    ptx::tmem_ld(row + Cf::T_OI + oc0 + 8 * j, y);
                     ptx::tmem_wait_ld();
                     ptx::tmem_pin(x);
                     ptx::tmem_pin(y);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2)
-                        ow[(g + i) / 2] = pack_bf16x2(fmaf(go, __uint_as_float(y[i]), a.scale * __uint_as_float(x[i])),
-                                                      fmaf(go, __uint_as_float(y[i + 1]), a.scale * __uint_as_float(x[i + 1])));
+                    for (int i = 0; i < 4; ++i)
+                        o[i] = keep & pack_bf16x2(fmaf(go, __uint_as_float(y[2 * i]), __uint_as_float(x[2 * i])),
+                                                  fmaf(go, __uint_as_float(y[2 * i + 1]), __uint_as_float(x[2 * i + 1])));
+                    *reinterpret_cast<uint4 *>(stg + swz_chunk<Cf::AW>(lane, j)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 ptx::tc_fence_before_sync();
+                ptx::fence_proxy_async_smem();
                 warp_arrive(one(B_OEMPTY), lane);
                 if (lane == 0) {
+                    // all of this chunk's products are done: K, V and (unless rows leave from it) Q are free
+                    ptx::mbar_arrive(empty(tk(c) % Cf::NSLOT));
                     ptx::mbar_arrive(empty(tv(c) % Cf::NSLOT));
-                    if (D != 128) {
-                        ptx::mbar_arrive(empty(tq(c) % Cf::NSLOT));
-                        ptx::bulk_wait_group_read<0>();  // the staged rows of the last chunk have left
-                    }
-                }
-                __syncwarp();
-                uint8_t *stg = D == 128 ? slot(tq(c)) + half * Cf::SUB + 32 * sub * Cf::ROWB
-                                        : base + Cf::OFF_O + 32 * sub * Cf::ROWB;
-#pragma unroll
-                for (int j = 0; j < OC / 8; ++j) {
-                    uint4 x = make_uint4(ow[4 * j], ow[4 * j + 1], ow[4 * j + 2], ow[4 * j + 3]);
-                    if (r >= n) x = make_uint4(0, 0, 0, 0);  // rows past the prompt's end are zeros
-                    *reinterpret_cast<uint4 *>(stg + swz_chunk<Cf::AW>(lane, j)) = x;
-                }
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    const MapCoord mc = map_coord(begin + c * Cf::C + 32 * sub, h, m.swap_o);
-                    if (begin + c * Cf::C + 32 * sub < a.N)
+                    if (D != 128) ptx::mbar_arrive(empty(tq(c) % Cf::NSLOT));
+                    const int n0 = begin + c * Cf::C + 32 * sub;
+                    const MapCoord mc = map_coord(n0, h, m.swap_o);
+                    if (n0 < a.N)
                         ptx::tma_store_4d_hint(&m.o, ptx::smem_u32(stg), oc0, mc.y, mc.z, b, ptx::l2_evict_first());
                     ptx::bulk_commit_group();
                 }
-                if (D == 128) {
-                    held = stg;
-                    held_slot = tq(c) % Cf::NSLOT;
-                }
+                held = tq(c) % Cf::NSLOT;
             }
         }
         if constexpr (STATES) {
@@ -530,17 +532,15 @@ __global__ void __launch_bounds__(DecayTc<D, STATES>::THREADS, D == 32 ? 2 : 1)
     if (end > begin) {
         const float lg = decay_log(a.log_decay, h);
         uint64_t *bars = reinterpret_cast<uint64_t *>(base + Cf::OFF_CTRL);
-        volatile int *flag = reinterpret_cast<volatile int *>(base + Cf::OFF_CTRL + 248);
-        uint32_t *tslot = reinterpret_cast<uint32_t *>(base + Cf::OFF_CTRL + 252);
+        uint32_t *tslot = reinterpret_cast<uint32_t *>(base + Cf::OFF_CTRL + 508);
         float *pw = reinterpret_cast<float *>(base + Cf::OFF_PW);
-        DecayUnit<D, STATES> u{a, base, bars, flag, pw, pw + 132, 0u, b, h, begin, end, lg, pool, wsp, seg};
+        DecayUnit<D, STATES> u{a, base, bars, pw, pw + 132, 0u, b, h, begin, end, lg, pool, wsp, seg};
         if (tid == 0) {
-            *flag = 0;
             u.init_barriers();
             ptx::fence_mbar_init();
         }
         if (tid < 129) pw[tid] = decay_pow(lg, (float)tid);
-        else if (tid < 161) pw[132 + tid - 129] = decay_pow(lg, (float)(31 - (tid - 129)));
+        else if (tid < 161) pw[132 + tid - 129] = a.scale * decay_pow(lg, (float)(31 - (tid - 129)));
         if (warp == 0) {
             ptx::tmem_alloc(ptx::smem_u32(tslot), Cf::TCOLS);
             ptx::tmem_relinquish();
@@ -558,7 +558,8 @@ __global__ void __launch_bounds__(DecayTc<D, STATES>::THREADS, D == 32 ? 2 : 1)
             u.states(m, warp - T, lane);
         } else if (lane == 0) {
             if (warp == U) u.producer(m);
-            else u.mma();
+            else if (STATES || warp == U + 1) u.mma_states();
+            else u.mma_outputs();
         }
         ptx::tc_fence_before_sync();
         __syncthreads();

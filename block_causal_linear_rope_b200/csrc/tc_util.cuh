@@ -32,6 +32,14 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
     return p + ((1024u - (a & 1023u)) & 1023u);
 }
 
+// mbar_wait_bounded for hand-overs that are usually a few hundred cycles away:
+// the warp suspends on the barrier at once, and the clock is read only after a
+// whole suspend time (10 ms) has passed, not on the way into every wait.
+__device__ __forceinline__ bool mbar_wait_patient(uint32_t bar, uint32_t parity, int *watchdog, int code) {
+    if (ptx::mbar_try_wait(bar, parity) || ptx::mbar_try_wait_suspend(bar, parity, ptx::kSuspendHintNs)) return true;
+    return ptx::mbar_wait_bounded(bar, parity, watchdog, code, kWaitLimitNs);
+}
+
 // One mbarrier arrival for the whole warp, after every lane's shared-memory
 // accesses (and tcgen05 loads, fenced by the caller) are ordered before it.
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
