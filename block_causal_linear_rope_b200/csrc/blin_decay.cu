@@ -47,10 +47,26 @@ cudaError_t launch_decay_simt(const DecayArgs &a, int d, cudaStream_t s) {
     return d == 32 ? simt<32>(a, s) : d == 64 ? simt<64>(a, s) : simt<128>(a, s);
 }
 
+// The warpgroups that take more registers draw on what the kernel was launched with: a build with fewer
+// than planned would leave them waiting, so it is not launched.
+template <auto Kernel>
+static bool has_registers(int n) {
+    static ContextCache<int> cache;
+    const unsigned long long ctx = current_context_id();
+    int have = 0;
+    if (!cache.get(ctx, &have)) {
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, Kernel) != cudaSuccess) return false;
+        cache.put(ctx, have = at.numRegs);
+    }
+    return have >= n;
+}
+
 template <int D>
 static cudaError_t tc(const DecayArgs &a, const DecayMaps &m, cudaStream_t s) {
     using CS = DecayTc<D, true>;
     using CO = DecayTc<D, false>;
+    if (CO::RSPLIT && !has_registers<decay_tc_kernel<D, false>>(CO::RL)) return cudaErrorInvalidConfiguration;
     return launch_prompt<decay_tc_kernel<D, true>, decay_tc_kernel<D, false>>(a, CS::THREADS, CS::BYTES, CO::THREADS,
                                                                              CO::BYTES, s, m);
 }

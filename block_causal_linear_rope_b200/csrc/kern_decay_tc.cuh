@@ -13,10 +13,10 @@
 // g^{n-1-j} v_j of its update are split into three bf16 parts (8 + 8 + 8 bits),
 // so that its product carries fp32 accuracy.
 //
-// Roles: a TMA producer thread, an MMA issuing thread, four warps that weight
-// the scores (TMEM -> registers -> P as bf16 over the scores in TMEM), four that
-// weight and split the values (shared memory -> shared memory), and four (d =
-// 128: eight) that own the state and the outputs.  They hand over through
+// Roles: a TMA producer thread, two MMA issuing threads (scores and outputs,
+// state), warpgroups that weight the scores (TMEM -> registers -> P as bf16 over
+// the scores in TMEM), that weight and split the values (shared memory -> shared
+// memory), and that own the state and the outputs.  They hand over through
 // mbarriers; every wait is bounded.
 //
 // A state product has only d rows.  Its A operand repeats the d features
@@ -37,8 +37,8 @@ struct DecayTc {
     static constexpr int ROWB = 2 * AW;
     static constexpr int SUB = C * ROWB, TILE = NAT * SUB;
     static constexpr uint32_t LAYOUT = D == 32 ? 4u : 2u;  // 64B / 128B swizzle
-    static constexpr int TPC = STATES ? 2 : 3;             // tiles landed per chunk: K, (Q,) V
-    static constexpr int NSLOT = D == 32 ? 9 : D == 64 ? 6 : 5;
+    static constexpr int TPC = STATES ? 2 : 3;             // tiles landed per chunk: V, K (, Q)
+    static constexpr int NSLOT = D == 128 ? 5 : 9;
     // weighted values: items of IT tokens, three parts each, in a ring of NVB
     static constexpr int IT = D == 128 ? 16 : 64, NIT = C / IT, NVB = 2;
     static constexpr int VSUB = IT * ROWB, VPART = NAT * VSUB, VITEM = 3 * VPART;
@@ -51,9 +51,12 @@ struct DecayTc {
     static constexpr int BYTES = OFF_PW + 4 * (132 + 32) + 1024;
     static_assert(8 * NBAR <= 504, "barriers");
     static_assert(BYTES <= 227 * 1024, "shared memory");
-    // warps
-    static constexpr int XW = STATES ? 0 : 4, TW = 4, UW = D == 128 ? 8 : 4;
-    static constexpr int THREADS = 32 * (XW + TW + UW + (STATES ? 2 : 3));
+    // Warps: XG and TG warpgroups share the scores and the values of a chunk; a d = 32 CTA has one of each,
+    // as two CTAs share an SM.  The last warpgroup holds the producer and the MMA threads.
+    static constexpr int XG = STATES ? 0 : D == 32 ? 1 : 2, TG = D == 32 ? 1 : 2, UW = D == 128 ? 8 : 4;
+    static constexpr int XW = 4 * XG, TW = 4 * TG;
+    static constexpr int THREADS = 32 * (XW + TW + UW + 4);
+    static constexpr int RELEASE = 8;  // arrivals that free a landing slot
     // TMEM columns: scores / P, inner and carried outputs, state product.  The three parts of the values
     // multiply side by side where there is room for a column range each (KVN = 3), else the low part is
     // added to the middle one's (2), or all to one (1).
@@ -62,6 +65,12 @@ struct DecayTc {
     static constexpr int TCOLS = STATES ? (D == 64 ? 256 : 128) : D == 32 ? 256 : 512;
     static_assert(T_KV + KVC <= TCOLS, "TMEM columns");
     static constexpr int NCOL = D == 128 ? 64 : D * D / 128;  // state columns per thread
+    // d = 128: 28 warps are launched with 72 registers a thread; the warpgroups that hold the state draw on
+    // what the others give up
+    static constexpr int RL = 72;
+    static constexpr bool RSPLIT = D == 128 && !STATES;
+    static constexpr int RX = RSPLIT ? 64 : 0, RT = RSPLIT ? 56 : 0, RU = RSPLIT ? 104 : 0, RC = RSPLIT ? 40 : 0;
+    static_assert(XW * RX + TW * RT + UW * RU + 4 * RC <= THREADS / 32 * RL, "registers");
 };
 
 // Maps and swaps of one call's operands.
@@ -102,21 +111,23 @@ struct DecayUnit {
     __device__ uint8_t *vbuf(int i) const { return base + Cf::OFF_V + (i % Cf::NVB) * Cf::VITEM; }
     __device__ uint8_t *sbuf(int c) const { return base + Cf::OFF_S + (c % Cf::NSB) * Cf::SIMG; }
     // tile numbers of chunk c in landing order
-    __device__ static int tk(int c) { return Cf::TPC * c; }
-    __device__ static int tq(int c) { return Cf::TPC * c + 1; }
-    __device__ static int tv(int c) { return Cf::TPC * c + Cf::TPC - 1; }
+    __device__ static int tv(int c) { return Cf::TPC * c; }
+    __device__ static int tk(int c) { return Cf::TPC * c + 1; }
+    __device__ static int tq(int c) { return Cf::TPC * c + 2; }
+    // `count` of the RELEASE arrivals that free tile t's slot
+    __device__ void release(int t, int count) const { ptx::mbar_arrive_n(empty(t % Cf::NSLOT), count); }
 
     __device__ void init_barriers() const {
         for (int s = 0; s < Cf::NSLOT; ++s) {
             ptx::mbar_init(full(s), 1);          // producer (+ bytes)
-            ptx::mbar_init(empty(s), Cf::UW);    // state / output warps
+            ptx::mbar_init(empty(s), Cf::RELEASE);
         }
         for (int s = 0; s < Cf::NVB; ++s) {
-            ptx::mbar_init(vready(s), Cf::TW);
+            ptx::mbar_init(vready(s), 4);
             ptx::mbar_init(vfree(s), 1);
         }
         ptx::mbar_init(one(B_SFULL), 1);
-        ptx::mbar_init(one(B_PREADY), 4);
+        ptx::mbar_init(one(B_PREADY), Cf::XW);
         ptx::mbar_init(one(B_KVFULL), 1);
         ptx::mbar_init(one(B_KVEMPTY), Cf::UW);
         ptx::mbar_init(one(B_SREADY), Cf::UW);
@@ -144,7 +155,7 @@ struct DecayUnit {
             for (int w = 0; w < Cf::TPC; ++w, ++t) {
                 const int s = t % Cf::NSLOT;
                 if (t >= Cf::NSLOT && !(ok = wait(empty(s), t / Cf::NSLOT - 1, WD_DC_EMPTY))) break;
-                const bool isv = w == Cf::TPC - 1, isk = w == 0;
+                const bool isv = w == 0, isk = w == 1;
                 const CUtensorMap *map = isk ? &m.k : isv ? &m.v : &m.q;
                 const MapCoord mc = map_coord(n, h, isk ? m.swap_k : isv ? m.swap_v : m.swap_q);
                 ptx::mbar_arrive_expect_tx(full(s), Cf::TILE);
@@ -196,7 +207,7 @@ struct DecayUnit {
             const uint64_t vd = mnmajor(ptx::smem_u32(slot(tv(c))), Cf::SUB);
 #pragma unroll
             for (int kk = 0; kk < Cf::C / 16; ++kk)
-                ptx::mma_bf16_ts(tmem + Cf::T_OA, tmem + 8 * kk, vd + static_cast<uint64_t>(kk * Cf::ROWB), IDO, kk > 0);
+                ptx::mma_bf16_ts(tmem + Cf::T_OA, tmem + 16 * kk, vd + static_cast<uint64_t>(kk * Cf::ROWB), IDO, kk > 0);
             ptx::mma_commit(one(B_OFULL));
         }
         drain();
@@ -207,6 +218,7 @@ struct DecayUnit {
         for (int c = 0; c < nc; ++c) {
             if (!wait(full(tk(c) % Cf::NSLOT), tk(c) / Cf::NSLOT, WD_DC_FULL)) break;
             if (c > 0 && !wait(one(B_KVEMPTY), c - 1, WD_DC_STATE)) break;
+            if (tokens(c) < Cf::C && !wait(one(B_CLEAN), 0, WD_DC_VALUE)) break;
             const uint64_t kd = mnmajor(ptx::smem_u32(slot(tk(c))), D == 128 ? Cf::SUB : 0);
             bool ok = true;
 #pragma unroll 1
@@ -245,19 +257,24 @@ struct DecayUnit {
     }
 
     // ------------------------------------------------------------ score warps (row i per thread)
-    // The weights scale g^{i-j} of the diagonal block stay in registers (0 right of the diagonal); left of
-    // it they are g^{i - 32 blk - 31} * scale g^{31 - (j - 32 blk)}, both powers >= 0.
-    __device__ void scores(int w, int lane) const {
+    // Columns go in groups of 16, which the XG warps of a row take in turn; a group's P (16 bf16) goes over
+    // the first half of its own columns.  The weights scale g^{i-j} of the diagonal block stay in registers
+    // (0 right of the diagonal); left of it they are g^{i - 32 blk - 31} * scale g^{31 - (j - 32 blk)}, both
+    // powers >= 0.
+    __device__ void scores(int xw, int lane) const {
+        constexpr int XG = Cf::XG == 2 ? 2 : 1, GS = 2 / XG;  // groups of a 32-column block that this warp takes
+        const int w = xw & 3, x0 = xw >> 2;
         const uint32_t row = tmem + (static_cast<uint32_t>(32 * w) << 16);
-        float dw[32];
+        float dw[16 * GS];
 #pragma unroll
-        for (int m = 0; m < 32; ++m) dw[m] = m <= lane ? a.scale * pw[lane - m] : 0.f;
+        for (int m = 0; m < 16 * GS; ++m) dw[m] = 16 * x0 + m <= lane ? a.scale * pw[lane - m - 16 * x0] : 0.f;
         const int nc = chunks();
         for (int c = 0; c < nc; ++c) {
             if (!wait(one(B_SFULL), c, WD_DC_SCORE)) break;
+            if (xw == 0 && lane == 0) release(tk(c), Cf::RELEASE / 2);  // multiplied by the queries
             ptx::tc_fence_after_sync();
 #pragma unroll 1
-            for (int g = 0; g < 2 * w; ++g) {  // 16 columns at a time
+            for (int g = x0; g < 2 * w; g += XG) {
                 uint32_t s[16], p[8];
                 ptx::tmem_ld(row + 16 * g, s);
                 const float f = pw[32 * (w - (g >> 1) - 1) + 1 + lane];
@@ -271,12 +288,13 @@ struct DecayUnit {
                     p[m / 2] = pack_bf16x2(x.x, x.y);
                     p[m / 2 + 1] = pack_bf16x2(y.x, y.y);
                 }
-                ptx::tmem_st(row + 8 * g, p);
+                ptx::tmem_st(row + 16 * g, p);
             }
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
+            for (int g = 0; g < GS; ++g) {
                 uint32_t s[16], p[8];
-                ptx::tmem_ld(row + 32 * w + 16 * g, s);
+                const uint32_t col = row + 32 * w + 16 * (x0 + g);
+                ptx::tmem_ld(col, s);
                 ptx::tmem_wait_ld();
                 ptx::tmem_pin(s);
 #pragma unroll
@@ -284,11 +302,11 @@ struct DecayUnit {
                     const float2 x = mul2(s[m], s[m + 1], make_float2(dw[16 * g + m], dw[16 * g + m + 1]));
                     p[m / 2] = pack_bf16x2(x.x, x.y);
                 }
-                ptx::tmem_st(row + 16 * w + 8 * g, p);
+                ptx::tmem_st(col, p);
             }
             const uint32_t zero[8] = {};
 #pragma unroll 1
-            for (int g = 2 * w + 2; g < 8; ++g) ptx::tmem_st(row + 8 * g, zero);
+            for (int g = 2 * w + 2 + x0; g < 8; g += XG) ptx::tmem_st(row + 16 * g, zero);
             ptx::tmem_wait_st();
             ptx::tc_fence_before_sync();
             warp_arrive(one(B_PREADY), lane);
@@ -305,9 +323,12 @@ struct DecayUnit {
     }
 
     // ------------------------------------------------------------ value warps
-    // Thread: one token row of an item, a share of its 16-byte pieces.
+    // Thread: one token row of an item, a share of its 16-byte pieces.  The TG warpgroups take the items in
+    // turn.
     __device__ void values(int tid, int lane) const {
         constexpr int PARTS = 128 / Cf::IT, PCS = D / 8 / PARTS;
+        const int tg = tid >> 7;
+        tid &= 127;
         const int r = tid % Cf::IT, part = tid / Cf::IT;
         const int nc = chunks();
         for (int c = 0; c < nc; ++c) {
@@ -318,17 +339,16 @@ struct DecayUnit {
                 // rows past the end multiply zeros: what lies there may be NaN
                 if (!wait(full(tk(c) % Cf::NSLOT), tk(c) / Cf::NSLOT, WD_DC_FULL)) return;
                 if (tid >= n)
-#pragma unroll
-                    for (int j = 0; j < Cf::NAT * (ROWP); ++j) {
+                    for (int j = 0; j < Cf::NAT * ROWP; ++j) {
                         const uint32_t off = (j / ROWP) * Cf::SUB + swz_chunk<Cf::AW>(tid, j % ROWP);
-                        *reinterpret_cast<uint4 *>(v + off) = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(slot(tk(c)) + off) = make_uint4(0, 0, 0, 0);
+                        if (tg == 0) *reinterpret_cast<uint4 *>(v + off) = make_uint4(0, 0, 0, 0);
+                        if (tg == Cf::TG - 1) *reinterpret_cast<uint4 *>(slot(tk(c)) + off) = make_uint4(0, 0, 0, 0);
                     }
                 ptx::fence_proxy_async_smem();
                 warp_arrive(one(B_CLEAN), lane);
             }
 #pragma unroll 1
-            for (int it = 0; it < Cf::NIT; ++it) {
+            for (int it = tg; it < Cf::NIT; it += Cf::TG) {
                 const int i = c * Cf::NIT + it, tok = it * Cf::IT + r;
                 if (i >= Cf::NVB && !wait(vfree(i % Cf::NVB), i / Cf::NVB - 1, WD_DC_VALUE)) return;
                 uint8_t *dst = vbuf(i);
@@ -401,7 +421,6 @@ struct DecayUnit {
         const DecaySplit whole(lg, (float)Cf::C);
         const float go = a.scale * pw[r + 1];
         const int nc = chunks();
-        int held = -1;  // d = 128: the Q slot this warp's last output rows leave from
         for (int c = 0; c < nc; ++c) {
             const int n = tokens(c);
             if (!wait(one(B_KVFULL), c, WD_DC_STATE)) break;
@@ -427,12 +446,11 @@ struct DecayUnit {
             }
             ptx::tc_fence_before_sync();
             warp_arrive(one(B_KVEMPTY), lane);
-            if constexpr (STATES) {
-                if (lane == 0) {
-                    ptx::mbar_arrive(empty(tk(c) % Cf::NSLOT));
-                    ptx::mbar_arrive(empty(tv(c) % Cf::NSLOT));
-                }
-            } else {
+            if (zw == 0 && lane == 0) {
+                release(tk(c), STATES ? Cf::RELEASE : Cf::RELEASE / 2);
+                if (STATES) release(tv(c), Cf::RELEASE);
+            }
+            if constexpr (!STATES) {
                 if (c + 1 < nc) {
                     // the next chunk's S image: with one buffer, once this chunk's has been multiplied
                     if (Cf::NSB == 1 && !wait(one(B_QSDONE), c, WD_DC_STATE)) break;
@@ -441,7 +459,7 @@ struct DecayUnit {
                 }
                 if (lane == 0 && c > 0) {  // the staged rows of the last chunk have left
                     ptx::bulk_wait_group_read<0>();
-                    if (D == 128) ptx::mbar_arrive(empty(held));
+                    if (D == 128) release(tq(c - 1), 1);
                 }
                 __syncwarp();
                 if (!wait(one(B_OFULL), c, WD_DC_OUT)) break;
@@ -452,34 +470,34 @@ struct DecayUnit {
                                         : base + Cf::OFF_O + 32 * sub * Cf::ROWB;
                 const uint32_t keep = r < n ? ~0u : 0u;  // rows past the prompt's end are zeros
 #pragma unroll 1
-                for (int j = 0; j < OC / 8; ++j) {
-                    uint32_t x[8], y[8], o[4];
+                for (int j = 0; j < OC / 8; j += 2) {
+                    uint32_t x[16], y[16], o[8];
                     ptx::tmem_ld(row + Cf::T_OA + oc0 + 8 * j, x);
                     ptx::tmem_ld(row + Cf::T_OI + oc0 + 8 * j, y);
                     ptx::tmem_wait_ld();
                     ptx::tmem_pin(x);
                     ptx::tmem_pin(y);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 8; ++i)
                         o[i] = keep & pack_bf16x2(fmaf(go, __uint_as_float(y[2 * i]), __uint_as_float(x[2 * i])),
                                                   fmaf(go, __uint_as_float(y[2 * i + 1]), __uint_as_float(x[2 * i + 1])));
                     *reinterpret_cast<uint4 *>(stg + swz_chunk<Cf::AW>(lane, j)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(stg + swz_chunk<Cf::AW>(lane, j + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
                 ptx::tc_fence_before_sync();
                 ptx::fence_proxy_async_smem();
                 warp_arrive(one(B_OEMPTY), lane);
                 if (lane == 0) {
-                    // all of this chunk's products are done: K, V and (unless rows leave from it) Q are free
-                    ptx::mbar_arrive(empty(tk(c) % Cf::NSLOT));
-                    ptx::mbar_arrive(empty(tv(c) % Cf::NSLOT));
-                    if (D != 128) ptx::mbar_arrive(empty(tq(c) % Cf::NSLOT));
+                    if (zw == 0) {  // all of this chunk's products are done: V and (unless rows leave from it) Q are free
+                        release(tv(c), Cf::RELEASE);
+                        if (D != 128) release(tq(c), Cf::RELEASE);
+                    }
                     const int n0 = begin + c * Cf::C + 32 * sub;
                     const MapCoord mc = map_coord(n0, h, m.swap_o);
                     if (n0 < a.N)
                         ptx::tma_store_4d_hint(&m.o, ptx::smem_u32(stg), oc0, mc.y, mc.z, b, ptx::l2_evict_first());
                     ptx::bulk_commit_group();
                 }
-                held = tq(c) % Cf::NSLOT;
             }
         }
         if constexpr (STATES) {
@@ -508,6 +526,13 @@ struct DecayUnit {
         ptx::fence_proxy_async_smem();
     }
 };
+
+// Registers a thread of this warpgroup may use from here on (0: as launched).
+template <int N>
+__device__ __forceinline__ void regs() {
+    if constexpr (N > 0 && N < DecayTc<128, false>::RL) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+    if constexpr (N > DecayTc<128, false>::RL) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 template <int D, bool STATES>
 __global__ void __launch_bounds__(DecayTc<D, STATES>::THREADS, D == 32 ? 2 : 1)
@@ -551,15 +576,21 @@ __global__ void __launch_bounds__(DecayTc<D, STATES>::THREADS, D == 32 ? 2 : 1)
         u.tmem = *tslot;
         constexpr int X = Cf::XW, T = X + Cf::TW, U = T + Cf::UW;
         if (warp < X) {
-            u.scores(warp, lane);
+            regs<Cf::RX>();
+            if constexpr (!STATES) u.scores(warp, lane);
         } else if (warp < T) {
+            regs<Cf::RT>();
             u.values(tid - 32 * X, lane);
         } else if (warp < U) {
+            regs<Cf::RU>();
             u.states(m, warp - T, lane);
-        } else if (lane == 0) {
-            if (warp == U) u.producer(m);
-            else if (STATES || warp == U + 1) u.mma_states();
-            else u.mma_outputs();
+        } else {
+            regs<Cf::RC>();
+            if (lane == 0) {
+                if (warp == U) u.producer(m);
+                else if (warp == U + 1) u.mma_states();
+                else if (!STATES && warp == U + 2) u.mma_outputs();
+            }
         }
         ptx::tc_fence_before_sync();
         __syncthreads();
