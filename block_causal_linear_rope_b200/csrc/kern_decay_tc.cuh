@@ -19,10 +19,14 @@
 // memory), and that own the state and the outputs.  They hand over through
 // mbarriers; every wait is bounded.
 //
-// A state product has only d rows.  Its A operand repeats the d features
-// (leading byte offset 0) up to the 128 lanes, and the lanes of each copy take a
-// share of the columns, so that all 128 threads of a warpgroup update the state.
+// Power.  The call is bound by memory in bytes, but the tensor cores' work alone
+// can take the card to its power limit and its clock down, so no product is
+// wider than it has to be: a state product has M = 64 rows at d <= 64 (d = 32
+// repeats its 32 features by a leading byte offset of 0, and the threads of each
+// copy take half of the columns).
 #pragma once
+
+#include <type_traits>
 
 #include "decay.cuh"
 #include "tc_util.cuh"
@@ -46,31 +50,35 @@ struct DecayTc {
     static constexpr int OSTG = STATES || D == 128 ? 0 : TILE;      // output staging (d = 128: in the chunk's Q slot)
     static constexpr int OFF_V = NSLOT * TILE, OFF_S = OFF_V + NVB * VITEM, OFF_O = OFF_S + (STATES ? 0 : NSB * SIMG);
     static constexpr int OFF_CTRL = OFF_O + OSTG;
-    static constexpr int NBAR = 2 * NSLOT + 2 * NVB + 11;
+    static constexpr int NBAR = 2 * NSLOT + 2 * NVB + 12;
     static constexpr int OFF_PW = OFF_CTRL + 512;  // g^n for n = 0 .. 128, then scale g^{31 - m} for m < 32
     static constexpr int BYTES = OFF_PW + 4 * (132 + 32) + 1024;
     static_assert(8 * NBAR <= 504, "barriers");
     static_assert(BYTES <= 227 * 1024, "shared memory");
-    // Warps: XG and TG warpgroups share the scores and the values of a chunk; a d = 32 CTA has one of each,
-    // as two CTAs share an SM.  The last warpgroup holds the producer and the MMA threads.
+    // Warps: XG and TG warpgroups share the scores and the values of a chunk, UW warps hold the state, ZW the
+    // outputs (0: the state's do both).  A d = 32 CTA has one warpgroup of each and no ZW, as two CTAs share an
+    // SM.  The last warpgroup holds the producer and the MMA threads.
     static constexpr int XG = STATES ? 0 : D == 32 ? 1 : 2, TG = D == 32 ? 1 : 2, UW = D == 128 ? 8 : 4;
-    static constexpr int XW = 4 * XG, TW = 4 * TG;
-    static constexpr int THREADS = 32 * (XW + TW + UW + 4);
-    static constexpr int RELEASE = 8;  // arrivals that free a landing slot
+    static constexpr int XW = 4 * XG, TW = 4 * TG, ZW = STATES || D == 32 ? 0 : 4, OW = ZW ? ZW : UW;
+    static constexpr int THREADS = 32 * (XW + TW + UW + ZW + 4);
+    static constexpr int RELEASE = 9;  // arrivals that free a landing slot
     // TMEM columns: scores / P, inner and carried outputs, state product.  The three parts of the values
     // multiply side by side where there is room for a column range each (KVN = 3), else the low part is
     // added to the middle one's (2), or all to one (1).
     static constexpr int KVN = D == 128 ? 1 : D == 64 || STATES ? 3 : 2, KVC = KVN * D;
+    static constexpr int KVM = D == 128 ? 128 : 64;  // rows of the state product
     static constexpr int T_OA = 128, T_OI = T_OA + D, T_KV = STATES ? 0 : T_OI + D;
     static constexpr int TCOLS = STATES ? (D == 64 ? 256 : 128) : D == 32 ? 256 : 512;
     static_assert(T_KV + KVC <= TCOLS, "TMEM columns");
     static constexpr int NCOL = D == 128 ? 64 : D * D / 128;  // state columns per thread
-    // d = 128: 28 warps are launched with 72 registers a thread; the warpgroups that hold the state draw on
-    // what the others give up
-    static constexpr int RL = 72;
-    static constexpr bool RSPLIT = D == 128 && !STATES;
-    static constexpr int RX = RSPLIT ? 64 : 0, RT = RSPLIT ? 56 : 0, RU = RSPLIT ? 104 : 0, RC = RSPLIT ? 40 : 0;
-    static_assert(XW * RX + TW * RT + UW * RU + 4 * RC <= THREADS / 32 * RL, "registers");
+    // d >= 64: the kernel is launched with RL registers a thread, and the warpgroups that hold the state or
+    // the outputs draw on what the others give up
+    static constexpr bool RSPLIT = D != 32 && !STATES;
+    static constexpr int RL = D == 128 ? 64 : 72;
+    static constexpr int RX = !RSPLIT ? 0 : D == 128 ? 56 : 64, RT = !RSPLIT ? 0 : D == 128 ? 48 : 56,
+                         RU = !RSPLIT ? 0 : D == 128 ? 96 : 112, RZ = !RSPLIT ? 0 : D == 128 ? 64 : 80,
+                         RC = !RSPLIT ? 0 : 40;
+    static_assert(XW * RX + TW * RT + UW * RU + ZW * RZ + 4 * RC <= THREADS / 32 * RL, "registers");
 };
 
 // Maps and swaps of one call's operands.
@@ -94,13 +102,13 @@ struct DecayUnit {
 
     // Barriers: full/empty of the landing slots, ready/free of the weighted values, then one each.  A wait
     // names a completion by its parity, so none may run two completions ahead of a role that waits for it:
-    //   B_SREADY   two barriers in turn: the states' chain may finish chunk c's product, and the image of
-    //              chunk c + 1 with it, before the outputs' thread asks for chunk c's image, but no further
-    //              (the next image waits for chunk c's outputs);
+    //   sready(c), qsdone(c)  two barriers in turn each where there are two state images: the states' chain
+    //              and the outputs' run up to an image apart;
     //   B_CLEAN    completes once, in a last chunk with rows past the prompt's end;
     //   all others are completed again only after what waits for them has passed.
-    enum { B_SFULL, B_PREADY, B_KVFULL, B_KVEMPTY, B_SREADY, B_SREADY1, B_QSDONE, B_OFULL, B_OEMPTY, B_CLEAN, B_DRAIN };
+    enum { B_SFULL, B_PREADY, B_KVFULL, B_KVEMPTY, B_SREADY, B_QSDONE = B_SREADY + 2, B_OFULL = B_QSDONE + 2, B_OEMPTY, B_CLEAN, B_DRAIN };
     __device__ uint32_t sready(int c) const { return one(B_SREADY + (c & 1)); }
+    __device__ uint32_t qsdone(int c) const { return one(B_QSDONE + (c & 1)); }
     __device__ uint32_t bar(int i) const { return ptx::smem_u32(bars + i); }
     __device__ uint32_t full(int s) const { return bar(s); }
     __device__ uint32_t empty(int s) const { return bar(Cf::NSLOT + s); }
@@ -114,7 +122,8 @@ struct DecayUnit {
     __device__ static int tv(int c) { return Cf::TPC * c; }
     __device__ static int tk(int c) { return Cf::TPC * c + 1; }
     __device__ static int tq(int c) { return Cf::TPC * c + 2; }
-    // `count` of the RELEASE arrivals that free tile t's slot
+    // `count` of the RELEASE arrivals that free tile t's slot: 8 by the warps that read it (K: the scores' for
+    // their product), 1 with the completion of the products that read it
     __device__ void release(int t, int count) const { ptx::mbar_arrive_n(empty(t % Cf::NSLOT), count); }
 
     __device__ void init_barriers() const {
@@ -131,11 +140,12 @@ struct DecayUnit {
         ptx::mbar_init(one(B_KVFULL), 1);
         ptx::mbar_init(one(B_KVEMPTY), Cf::UW);
         ptx::mbar_init(one(B_SREADY), Cf::UW);
-        ptx::mbar_init(one(B_SREADY1), Cf::UW);
+        ptx::mbar_init(one(B_SREADY + 1), Cf::UW);
         ptx::mbar_init(one(B_CLEAN), Cf::TW);
         ptx::mbar_init(one(B_QSDONE), 1);
+        ptx::mbar_init(one(B_QSDONE + 1), 1);
         ptx::mbar_init(one(B_OFULL), 1);
-        ptx::mbar_init(one(B_OEMPTY), Cf::UW);
+        ptx::mbar_init(one(B_OEMPTY), Cf::OW);
         ptx::mbar_init(one(B_DRAIN), STATES ? 1 : 2);
     }
     // Waits for completion number `k` (from 0) of a barrier; false: gave up.  A role that gives up stops,
@@ -201,7 +211,7 @@ struct DecayUnit {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
                 ptx::mma_bf16_ss(tmem + Cf::T_OI, qd + kstep(kk), sd + static_cast<uint64_t>(kk * Cf::ROWB), IDO, kk > 0);
-            if (Cf::NSB == 1) ptx::mma_commit(one(B_QSDONE));
+            if (Cf::ZW) ptx::mma_commit(qsdone(c));
             if (!wait(full(tv(c) % Cf::NSLOT), tv(c) / Cf::NSLOT, WD_DC_FULL) || !wait(one(B_PREADY), c, WD_DC_SCORE)) break;
             ptx::tc_fence_after_sync();
             const uint64_t vd = mnmajor(ptx::smem_u32(slot(tv(c))), Cf::SUB);
@@ -209,6 +219,13 @@ struct DecayUnit {
             for (int kk = 0; kk < Cf::C / 16; ++kk)
                 ptx::mma_bf16_ts(tmem + Cf::T_OA, tmem + 16 * kk, vd + static_cast<uint64_t>(kk * Cf::ROWB), IDO, kk > 0);
             ptx::mma_commit(one(B_OFULL));
+            ptx::mma_commit(empty(tv(c) % Cf::NSLOT));
+            if (D == 128) {
+                release(tq(c), 1);  // and by the warps whose rows leave from it
+            } else {
+                release(tq(c), Cf::RELEASE - 1);
+                ptx::mma_commit(empty(tq(c) % Cf::NSLOT));
+            }
         }
         drain();
     }
@@ -232,7 +249,7 @@ struct DecayUnit {
                 for (int kk = 0; kk < Cf::IT / 16; ++kk) {
                     const uint64_t bo = static_cast<uint64_t>(kk * Cf::ROWB);
                     const uint32_t acc = it > 0 || kk > 0;
-                    constexpr uint32_t ID = ptx::idesc_bf16_f32(128, Cf::KVN * D, 1, 1), ID1 = ptx::idesc_bf16_f32(128, D, 1, 1);
+                    constexpr uint32_t ID = ptx::idesc_bf16_f32(Cf::KVM, Cf::KVN * D, 1, 1), ID1 = ptx::idesc_bf16_f32(Cf::KVM, D, 1, 1);
                     if constexpr (Cf::KVN == 1) {  // small parts first
 #pragma unroll
                         for (int part = 2; part >= 0; --part)
@@ -247,6 +264,11 @@ struct DecayUnit {
             }
             if (!ok) break;
             ptx::mma_commit(one(B_KVFULL));
+            ptx::mma_commit(empty(tk(c) % Cf::NSLOT));
+            if (STATES) {
+                release(tk(c), Cf::RELEASE - 1);
+                release(tv(c), 1);
+            }
         }
         drain();
     }
@@ -271,7 +293,7 @@ struct DecayUnit {
         const int nc = chunks();
         for (int c = 0; c < nc; ++c) {
             if (!wait(one(B_SFULL), c, WD_DC_SCORE)) break;
-            if (xw == 0 && lane == 0) release(tk(c), Cf::RELEASE / 2);  // multiplied by the queries
+            if (xw == 0 && lane == 0) release(tk(c), Cf::RELEASE - 1);  // multiplied by the queries
             ptx::tc_fence_after_sync();
 #pragma unroll 1
             for (int g = x0; g < 2 * w; g += XG) {
@@ -373,6 +395,7 @@ struct DecayUnit {
                 ptx::fence_proxy_async_smem();  // written for the MMA; V read before its slot is filled again
                 warp_arrive(vready(i % Cf::NVB), lane);
             }
+            if (lane == 0) release(tv(c), 8 / Cf::TW);
         }
     }
     static constexpr int ROWP = Cf::ROWB / 16;  // 16-byte pieces of a row of one atom
@@ -391,147 +414,201 @@ struct DecayUnit {
                            v.y - __uint_as_float(__float_as_uint(v.y) & 0xFFFF0000u));
     }
 
-    // ------------------------------------------------------------ state and output warps
-    __device__ void states(const DecayMaps &m, int zw, int lane) const {
-        constexpr int NCOL = Cf::NCOL;
-        const int sub = zw & 3, half = zw >> 2, r = 32 * sub + lane, f = r % D;
-        const int col0 = D == 128 ? 64 * half : (r / D) * NCOL;
-        const uint32_t row = tmem + (static_cast<uint32_t>(32 * sub) << 16);
-        float st[NCOL];
-#pragma unroll
-        for (int i = 0; i < NCOL; ++i) st[i] = 0.f;
-        if constexpr (!STATES) {
-            auto add = [&](const float *src, float w) {
-                const float4 *p = reinterpret_cast<const float4 *>(src + (size_t)f * D + col0);
-#pragma unroll
-                for (int i = 0; i < NCOL / 4; ++i) {
-                    const float4 x = p[i];
-                    st[4 * i] = fmaf(w, x.x, st[4 * i]);
-                    st[4 * i + 1] = fmaf(w, x.y, st[4 * i + 1]);
-                    st[4 * i + 2] = fmaf(w, x.z, st[4 * i + 2]);
-                    st[4 * i + 3] = fmaf(w, x.w, st[4 * i + 3]);
-                }
-            };
-            if (a.nseg > 1)
-                for (int s = 0; s <= seg; ++s) add(wsp + (size_t)s * D * D, decay_pow(lg, (float)(begin - s * a.seg)));
-            else if (pool) add(pool, 1.f);
-            put_state(st, f, col0, sbuf(0));
-            warp_arrive(sready(0), lane);
-        }
-        const DecaySplit whole(lg, (float)Cf::C);
-        const float go = a.scale * pw[r + 1];
-        const int nc = chunks();
-        for (int c = 0; c < nc; ++c) {
-            const int n = tokens(c);
-            if (!wait(one(B_KVFULL), c, WD_DC_STATE)) break;
-            ptx::tc_fence_after_sync();
-            DecaySplit g = whole;
-            if (n < Cf::C) g = DecaySplit(lg, (float)n);
-            constexpr int W = 8;
-#pragma unroll
-            for (int i0 = 0; i0 < NCOL; i0 += W) {
-                uint32_t x[Cf::KVN][W];
-#pragma unroll
-                for (int p = 0; p < Cf::KVN; ++p) ptx::tmem_ld(row + Cf::T_KV + p * D + col0 + i0, x[p]);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int p = 0; p < Cf::KVN; ++p) ptx::tmem_pin(x[p]);
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    float t = __uint_as_float(x[Cf::KVN - 1][i]);
-#pragma unroll
-                    for (int p = Cf::KVN - 2; p >= 0; --p) t += __uint_as_float(x[p][i]);
-                    st[i0 + i] = fmaf(st[i0 + i], g.hi, fmaf(st[i0 + i], g.lo, t));
-                }
-            }
-            ptx::tc_fence_before_sync();
-            warp_arrive(one(B_KVEMPTY), lane);
-            if (zw == 0 && lane == 0) {
-                release(tk(c), STATES ? Cf::RELEASE : Cf::RELEASE / 2);
-                if (STATES) release(tv(c), Cf::RELEASE);
-            }
-            if constexpr (!STATES) {
-                if (c + 1 < nc) {
-                    // the next chunk's S image: with one buffer, once this chunk's has been multiplied
-                    if (Cf::NSB == 1 && !wait(one(B_QSDONE), c, WD_DC_STATE)) break;
-                    put_state(st, f, col0, sbuf(c + 1));
-                    warp_arrive(sready(c + 1), lane);
-                }
-                if (lane == 0 && c > 0) {  // the staged rows of the last chunk have left
-                    ptx::bulk_wait_group_read<0>();
-                    if (D == 128) release(tq(c - 1), 1);
-                }
-                __syncwarp();
-                if (!wait(one(B_OFULL), c, WD_DC_OUT)) break;
-                ptx::tc_fence_after_sync();
-                constexpr int OC = D == 128 ? 64 : D;  // output columns of this thread
-                const int oc0 = D == 128 ? col0 : 0;
-                uint8_t *stg = D == 128 ? slot(tq(c)) + half * Cf::SUB + 32 * sub * Cf::ROWB
-                                        : base + Cf::OFF_O + 32 * sub * Cf::ROWB;
-                const uint32_t keep = r < n ? ~0u : 0u;  // rows past the prompt's end are zeros
-#pragma unroll 1
-                for (int j = 0; j < OC / 8; j += 2) {
-                    uint32_t x[16], y[16], o[8];
-                    ptx::tmem_ld(row + Cf::T_OA + oc0 + 8 * j, x);
-                    ptx::tmem_ld(row + Cf::T_OI + oc0 + 8 * j, y);
-                    ptx::tmem_wait_ld();
-                    ptx::tmem_pin(x);
-                    ptx::tmem_pin(y);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        o[i] = keep & pack_bf16x2(fmaf(go, __uint_as_float(y[2 * i]), __uint_as_float(x[2 * i])),
-                                                  fmaf(go, __uint_as_float(y[2 * i + 1]), __uint_as_float(x[2 * i + 1])));
-                    *reinterpret_cast<uint4 *>(stg + swz_chunk<Cf::AW>(lane, j)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(stg + swz_chunk<Cf::AW>(lane, j + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-                }
-                ptx::tc_fence_before_sync();
-                ptx::fence_proxy_async_smem();
-                warp_arrive(one(B_OEMPTY), lane);
-                if (lane == 0) {
-                    if (zw == 0) {  // all of this chunk's products are done: V and (unless rows leave from it) Q are free
-                        release(tv(c), Cf::RELEASE);
-                        if (D != 128) release(tq(c), Cf::RELEASE);
-                    }
-                    const int n0 = begin + c * Cf::C + 32 * sub;
-                    const MapCoord mc = map_coord(n0, h, m.swap_o);
-                    if (n0 < a.N)
-                        ptx::tma_store_4d_hint(&m.o, ptx::smem_u32(stg), oc0, mc.y, mc.z, b, ptx::l2_evict_first());
-                    ptx::bulk_commit_group();
-                }
+    // ------------------------------------------------------------ state warps
+    // Elements of the state a thread holds.  d = 128: row f = 32 sub + lane, 64 columns from col0.  Else the
+    // 16-lane fragments of an M = 64 product: pairs of neighbouring columns, pair p in row f + 8 (p & 1) and
+    // column col0 + 8 (p >> 1) + 2 (lane & 3).
+    struct Piece {
+        uint32_t row;  // TMEM lanes of this warp
+        int f, col0;
+        __device__ Piece(uint32_t tmem, int uw, int lane) {
+            const int sub = uw & 3;
+            row = tmem + (static_cast<uint32_t>(32 * sub) << 16);
+            if constexpr (D == 128) {
+                f = 32 * sub + lane;
+                col0 = 64 * (uw >> 2);
+            } else {
+                f = (16 * sub + (lane >> 2)) % D;
+                col0 = (16 * sub / D) * 16;
             }
         }
-        if constexpr (STATES) {
-            store_state(st, wsp + (size_t)(seg + 1) * D * D, f, col0);
-        } else {
-            if (pool && end > begin && !more()) store_state(st, pool, f, col0);
-            if (lane == 0) ptx::bulk_wait_group_read<0>();  // staged rows have left before the CTA's memory goes
+        static constexpr int RUN = D == 128 ? 4 : 2;  // elements of one access to a row in memory
+        __device__ int offset(int i, int lane) const {
+            if constexpr (D == 128) return f * D + col0 + RUN * i;
+            else return (f + 8 * (i & 1)) * D + col0 + 8 * (i >> 1) + 2 * (lane & 3);
         }
+    };
+    using Run = typename std::conditional<D == 128, float4, float2>::type;
+
+    __device__ void load_state(float (&st)[Cf::NCOL], const Piece &pc, int lane) const {
+        auto add = [&](const float *src, float w) {
+#pragma unroll
+            for (int i = 0; i < Cf::NCOL / Piece::RUN; ++i) {
+                const Run x = *reinterpret_cast<const Run *>(src + pc.offset(i, lane));
+                const float *e = &x.x;
+#pragma unroll
+                for (int u = 0; u < Piece::RUN; ++u) st[Piece::RUN * i + u] = fmaf(w, e[u], st[Piece::RUN * i + u]);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < Cf::NCOL; ++i) st[i] = 0.f;
+        if (a.nseg > 1)
+            for (int s = 0; s <= seg; ++s) add(wsp + (size_t)s * D * D, decay_pow(lg, (float)(begin - s * a.seg)));
+        else if (pool) add(pool, 1.f);
     }
-    // whether the prompt goes on behind this segment
-    __device__ bool more() const { return end < decay_len(a, b); }
-    __device__ static void store_state(const float (&st)[Cf::NCOL], float *dst, int f, int col0) {
-        float4 *p = reinterpret_cast<float4 *>(dst + (size_t)f * D + col0);
+    __device__ static void store_state(const float (&st)[Cf::NCOL], float *dst, const Piece &pc, int lane) {
 #pragma unroll
-        for (int i = 0; i < Cf::NCOL / 4; ++i) p[i] = make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
+        for (int i = 0; i < Cf::NCOL / Piece::RUN; ++i) {
+            Run x;
+            float *e = &x.x;
+#pragma unroll
+            for (int u = 0; u < Piece::RUN; ++u) e[u] = st[Piece::RUN * i + u];
+            *reinterpret_cast<Run *>(dst + pc.offset(i, lane)) = x;
+        }
     }
     // this thread's part of the state as a bf16 operand image
-    __device__ static void put_state(const float (&st)[Cf::NCOL], int f, int col0, uint8_t *img) {
+    __device__ static void put_state(const float (&st)[Cf::NCOL], uint8_t *img, const Piece &pc, int lane) {
+        if constexpr (D == 128) {
 #pragma unroll
-        for (int j = 0; j < Cf::NCOL / 8; ++j) {
-            const int pc = col0 / 8 + j;
-            const float *s = st + 8 * j;
-            *reinterpret_cast<uint4 *>(img + (pc / ROWP) * D * Cf::ROWB + swz_chunk<Cf::AW>(f, pc % ROWP)) = make_uint4(
-                pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+            for (int j = 0; j < Cf::NCOL / 8; ++j) {
+                const int q = pc.col0 / 8 + j;
+                const float *s = st + 8 * j;
+                *reinterpret_cast<uint4 *>(img + (q / ROWP) * D * Cf::ROWB + swz_chunk<Cf::AW>(pc.f, q % ROWP)) =
+                    make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < Cf::NCOL / 2; ++p)
+                *reinterpret_cast<uint32_t *>(img + swz_chunk<Cf::AW>(pc.f + 8 * (p & 1), pc.col0 / 8 + (p >> 1)) + 4 * (lane & 3)) =
+                    pack_bf16x2(st[2 * p], st[2 * p + 1]);
         }
         ptx::fence_proxy_async_smem();
     }
+    // S <- g S + this chunk's product
+    __device__ void add_product(float (&st)[Cf::NCOL], const DecaySplit &g, const Piece &pc) const {
+#pragma unroll
+        for (int i0 = 0; i0 < Cf::NCOL; i0 += 8) {
+            uint32_t x[Cf::KVN][8];
+            const int col = D == 128 ? i0 : 2 * i0;  // 8 columns of a row, or 16 columns of two half rows
+#pragma unroll
+            for (int p = 0; p < Cf::KVN; ++p) {
+                const uint32_t at = pc.row + Cf::T_KV + p * D + pc.col0 + col;
+                if constexpr (D == 128) ptx::tmem_ld(at, x[p]);
+                else ptx::tmem_ld_16x256(at, x[p]);
+            }
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int p = 0; p < Cf::KVN; ++p) ptx::tmem_pin(x[p]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float t = __uint_as_float(x[Cf::KVN - 1][i]);
+#pragma unroll
+                for (int p = Cf::KVN - 2; p >= 0; --p) t += __uint_as_float(x[p][i]);
+                st[i0 + i] = fmaf(st[i0 + i], g.hi, fmaf(st[i0 + i], g.lo, t));
+            }
+        }
+    }
+    __device__ void states(const DecayMaps &m, int uw, int lane) const {
+        const Piece pc(tmem, uw, lane);
+        float st[Cf::NCOL];
+        if constexpr (STATES) {
+#pragma unroll
+            for (int i = 0; i < Cf::NCOL; ++i) st[i] = 0.f;
+        } else {
+            load_state(st, pc, lane);
+            put_state(st, sbuf(0), pc, lane);
+            warp_arrive(sready(0), lane);
+        }
+        const DecaySplit whole(lg, (float)Cf::C);
+        const int nc = chunks();
+        bool ok = true;
+        for (int c = 0; c < nc && ok; ++c) {
+            const int n = tokens(c);
+            if (!(ok = wait(one(B_KVFULL), c, WD_DC_STATE))) break;
+            ptx::tc_fence_after_sync();
+            DecaySplit g = whole;
+            if (n < Cf::C) g = DecaySplit(lg, (float)n);
+            add_product(st, g, pc);
+            ptx::tc_fence_before_sync();
+            warp_arrive(one(B_KVEMPTY), lane);
+            if constexpr (!STATES) {
+                if (c + 1 < nc) {
+                    // the next chunk's image goes where that of chunk c + 1 - NSB was: multiplied by now (without
+                    // output warps this warp has seen that chunk's outputs)
+                    const int u = c + 1 - Cf::NSB;
+                    if (Cf::ZW && u >= 0 && !(ok = wait(qsdone(u), u >> 1, WD_DC_STATE))) break;
+                    put_state(st, sbuf(c + 1), pc, lane);
+                    warp_arrive(sready(c + 1), lane);
+                }
+                if (!Cf::ZW) ok = output_chunk(m, c, uw, lane);
+            }
+        }
+        if constexpr (STATES) {
+            store_state(st, wsp + (size_t)(seg + 1) * D * D, pc, lane);
+        } else {
+            if (ok && pool && end == decay_len(a, b)) store_state(st, pool, pc, lane);
+            if (!Cf::ZW && lane == 0) ptx::bulk_wait_group_read<0>();
+        }
+    }
+
+    // ------------------------------------------------------------ output warps (row i per thread)
+    __device__ void outputs(const DecayMaps &m, int zw, int lane) const {
+        const int nc = chunks();
+        for (int c = 0; c < nc; ++c)
+            if (!output_chunk(m, c, zw, lane)) break;
+        if (lane == 0) ptx::bulk_wait_group_read<0>();  // staged rows have left before the CTA's memory goes
+    }
+    __device__ bool output_chunk(const DecayMaps &m, int c, int sub, int lane) const {
+        const int r = 32 * sub + lane, n = tokens(c);
+        const float go = a.scale * pw[r + 1];
+        const uint32_t row = tmem + (static_cast<uint32_t>(32 * sub) << 16);
+        if (lane == 0 && c > 0) {  // the staged rows of the last chunk have left
+            ptx::bulk_wait_group_read<0>();
+            if (D == 128) release(tq(c - 1), 8 / Cf::OW);
+        }
+        __syncwarp();
+        if (!wait(one(B_OFULL), c, WD_DC_OUT)) return false;
+        ptx::tc_fence_after_sync();
+        uint8_t *stg = (D == 128 ? slot(tq(c)) : base + Cf::OFF_O) + 32 * sub * Cf::ROWB;
+        const uint32_t keep = r < n ? ~0u : 0u;  // rows past the prompt's end are zeros
+#pragma unroll 1
+        for (int j = 0; j < D / 8; j += 2) {
+            uint32_t x[16], y[16], o[8];
+            ptx::tmem_ld(row + Cf::T_OA + 8 * j, x);
+            ptx::tmem_ld(row + Cf::T_OI + 8 * j, y);
+            ptx::tmem_wait_ld();
+            ptx::tmem_pin(x);
+            ptx::tmem_pin(y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                o[i] = keep & pack_bf16x2(fmaf(go, __uint_as_float(y[2 * i]), __uint_as_float(x[2 * i])),
+                                          fmaf(go, __uint_as_float(y[2 * i + 1]), __uint_as_float(x[2 * i + 1])));
+            uint8_t *dst = stg + (j / ROWP) * Cf::SUB;
+            *reinterpret_cast<uint4 *>(dst + swz_chunk<Cf::AW>(lane, j % ROWP)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(dst + swz_chunk<Cf::AW>(lane, j % ROWP + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        ptx::tc_fence_before_sync();
+        ptx::fence_proxy_async_smem();
+        warp_arrive(one(B_OEMPTY), lane);
+        if (lane == 0) {
+            const int n0 = begin + c * Cf::C + 32 * sub;
+            const MapCoord mc = map_coord(n0, h, m.swap_o);
+            if (n0 < a.N)
+#pragma unroll
+                for (int at = 0; at < Cf::NAT; ++at)
+                    ptx::tma_store_4d_hint(&m.o, ptx::smem_u32(stg + at * Cf::SUB), at * Cf::AW, mc.y, mc.z, b,
+                                           ptx::l2_evict_first());
+            ptx::bulk_commit_group();
+        }
+        return true;
+    }
 };
 
-// Registers a thread of this warpgroup may use from here on (0: as launched).
-template <int N>
+// Changes the registers a thread of this warpgroup may use from FROM to TO (0: no split).
+template <int FROM, int TO>
 __device__ __forceinline__ void regs() {
-    if constexpr (N > 0 && N < DecayTc<128, false>::RL) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-    if constexpr (N > DecayTc<128, false>::RL) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    if constexpr (FROM > 0 && TO > 0 && TO < FROM) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TO));
+    if constexpr (FROM > 0 && TO > 0 && TO > FROM) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TO));
 }
 
 template <int D, bool STATES>
@@ -574,23 +651,32 @@ __global__ void __launch_bounds__(DecayTc<D, STATES>::THREADS, D == 32 ? 2 : 1)
         __syncthreads();
         ptx::tc_fence_after_sync();
         u.tmem = *tslot;
-        constexpr int X = Cf::XW, T = X + Cf::TW, U = T + Cf::UW;
+        constexpr int X = Cf::XW, T = X + Cf::TW, U = T + Cf::UW, Z = U + Cf::ZW, RL = Cf::RL;
         if (warp < X) {
-            regs<Cf::RX>();
+            regs<RL, Cf::RX>();
             if constexpr (!STATES) u.scores(warp, lane);
+            regs<Cf::RX, RL>();  // the code behind the roles is common to all
         } else if (warp < T) {
-            regs<Cf::RT>();
+            regs<RL, Cf::RT>();
             u.values(tid - 32 * X, lane);
+            regs<Cf::RT, RL>();
         } else if (warp < U) {
-            regs<Cf::RU>();
+            regs<RL, Cf::RU>();
             u.states(m, warp - T, lane);
+            regs<Cf::RU, RL>();
+        } else if (warp < Z) {
+            regs<RL, Cf::RZ>();
+            if constexpr (Cf::ZW > 0) u.outputs(m, warp - U, lane);
+            regs<Cf::RZ, RL>();
         } else {
-            regs<Cf::RC>();
+            regs<RL, Cf::RC>();
             if (lane == 0) {
-                if (warp == U) u.producer(m);
-                else if (warp == U + 1) u.mma_states();
-                else if (!STATES && warp == U + 2) u.mma_outputs();
+                if (warp == Z) u.producer(m);
+                else if (warp == Z + 1) u.mma_states();
+                else if (!STATES && warp == Z + 2) u.mma_outputs();
             }
+            __syncwarp();
+            regs<Cf::RC, RL>();
         }
         ptx::tc_fence_before_sync();
         __syncthreads();

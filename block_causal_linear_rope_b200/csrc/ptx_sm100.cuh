@@ -307,6 +307,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr)
         : "memory");
 }
+// 16 columns of the first 16 lanes of this warp's TMEM quarter (16x256b shape):
+// registers 4g + {0, 1} hold columns 8g + 2 (t % 4) + {0, 1} of lane t / 4, and
+// 4g + {2, 3} the same columns of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void tmem_pin(uint32_t (&r)[N]) {
