@@ -132,6 +132,7 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+from . import _blin_torch as _ext  # noqa: E402  (built next to the library; links it)
 
 
 def _check(status: int) -> None:
@@ -603,58 +604,20 @@ def block_step_nvfp4(q: Nvfp4Tensor, k: Nvfp4Tensor, v: Nvfp4Tensor, Hg: int, Wg
 
 
 # ----------------------------------------------------------------------------- decayed linear attention
-def _check_operand(name: str, t, shape, dtype, device) -> None:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.shape != shape or t.dtype != dtype or t.device != device or t.stride(-1) != 1:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}, last dimension contiguous "
-                         f"(got {t.dtype}, {tuple(t.shape)}, {t.device}, strides {t.stride()})")
+# These calls run for a few microseconds: their arguments are checked and handed to the library by
+# the extension next to it (csrc/blin_torch.cpp), which returns the output or the library's status.
+def _result(r):
+    if type(r) is int:
+        _check(r)
+    return r
 
 
-def _check_index(name: str, t, n: int, device) -> Optional[int]:
-    """Address of an optional int32 [n] tensor."""
-    if t is None:
-        return None
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.dim() != 1
-            or t.shape[0] != n or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on {device}")
-    return t.data_ptr()
-
-
-def _check_log_decay(t, H: int, device) -> int:
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device or t.dim() != 1
-            or t.shape[0] != H or not t.is_contiguous()):
-        raise ValueError(f"log_decay must be a contiguous float32 [{H}] tensor on {device}")
-    return t.data_ptr()
-
-
-def _check_pool(state, H: int, d: int, device) -> int:
-    """Slots of a state pool."""
-    if (not isinstance(state, torch.Tensor) or state.dtype != torch.float32 or state.device != device or state.dim() != 4
-            or state.shape[1:] != (H, d, d) or not state.is_contiguous()):
-        raise ValueError(f"state must be a contiguous float32 [slots, {H}, {d}, {d}] tensor on {device}")
-    return state.shape[0]
-
-
-def _layout(t: torch.Tensor) -> Layout:
-    """Strides of a [B, H, N, d] or [B, H, d] tensor (the latter has no token stride)."""
-    st = t.stride()
-    return Layout(st[2] if len(st) == 4 else t.shape[-1], st[1], st[0])
-
-
-def _on_stream(stream, *tensors) -> int:
-    """Handle of the call's stream; memory allocated here on the current stream is kept until a
-    different one has used it."""
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def decay_workspace_size(B: int, H: int, N: int, d: int, dtype: torch.dtype = torch.bfloat16) -> int:
-    """Workspace bytes of decay_prefill for this shape."""
+    """Workspace bytes of decay_prefill for this shape (at most 16: it needs none)."""
     n = int(lib.blin_decay_workspace_size(B, H, N, d, BF16 if dtype == torch.bfloat16 else F32))
     if n == 0:
         raise ValueError("invalid shape for blin_decay_prefill: " + lib.blin_last_error().decode())
@@ -675,38 +638,7 @@ def decay_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: 
     row's slot (None: row b uses slot b); a negative entry marks an idle row, whose outputs are
     zeros.  `lengths`, int32 [B], gives each row's tokens (None: all N); outputs past them are
     zeros."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be a [B, H, N, d] tensor")
-    B, H, N, d = q.shape
-    dt, dev = _dtype_code(q), q.device
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _check_operand(name, t, q.shape, q.dtype, dev)
-    _check_device(q)
-    lg = _check_log_decay(log_decay, H, dev)
-    n_slots = 0 if state is None else _check_pool(state, H, d, dev)
-    slot_ptr, len_ptr = _check_index("slots", slots, B, dev), _check_index("lengths", lengths, B, dev)
-    made = None
-    if out is None:
-        made = out = torch.empty((B, H, N, d), dtype=q.dtype, device=dev)
-    else:
-        _check_out(out, q.shape, q.dtype, dev)
-        _check_no_overlap(out, q, k, v, *(() if state is None else (state,)))
-    if N == 0:
-        return out
-    need = int(lib.blin_decay_workspace_size(B, H, N, d, dt))
-    scratch, ws_ptr, ws_bytes = None, None, 0
-    if workspace is not None:
-        workspace, ws_ptr, ws_bytes = _workspace_arg(workspace, need, dev)
-    elif need > 16:
-        scratch = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws_ptr, ws_bytes = scratch.data_ptr(), need
-    lay = None
-    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()):
-        lay = ctypes.byref(DecayLayouts(_layout(q), _layout(k), _layout(v), _layout(out)))
-    _check(lib.blin_decay_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dt, B, H, N, d, lg, scale,
-                                  lay, len_ptr, None if state is None else state.data_ptr(), n_slots, slot_ptr, ws_ptr,
-                                  ws_bytes, _on_stream(stream, made, scratch)))
-    return out
+    return _result(_ext.decay_prefill(q, k, v, log_decay, state, slots, lengths, scale, out, workspace, _handle(stream)))
 
 
 def decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, state: torch.Tensor,
@@ -714,27 +646,7 @@ def decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: tor
                stream=None) -> torch.Tensor:
     """decay_prefill() for one token per row: q, k, v and the output are [B, H, d].  Reads and
     updates the rows' states in the pool (see decay_prefill)."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a [B, H, d] tensor")
-    B, H, d = q.shape
-    dt, dev = _dtype_code(q), q.device
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _check_operand(name, t, q.shape, q.dtype, dev)
-    _check_device(q)
-    lg = _check_log_decay(log_decay, H, dev)
-    n_slots, slot_ptr = _check_pool(state, H, d, dev), _check_index("slots", slots, B, dev)
-    made = None
-    if out is None:
-        made = out = torch.empty((B, H, d), dtype=q.dtype, device=dev)
-    else:
-        _check_out(out, q.shape, q.dtype, dev)
-        _check_no_overlap(out, q, k, v, state)
-    lay = None
-    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()):
-        lay = ctypes.byref(DecayLayouts(_layout(q), _layout(k), _layout(v), _layout(out)))
-    _check(lib.blin_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dt, B, H, d, lg, scale, lay,
-                               state.data_ptr(), n_slots, slot_ptr, _on_stream(stream, made)))
-    return out
+    return _result(_ext.decay_step(q, k, v, log_decay, state, slots, scale, out, _handle(stream)))
 
 
 # ----------------------------------------------------------------------------- rotary embedding
@@ -750,43 +662,4 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, rope_split: Seque
     rope(g, inverse=True) takes an output's gradient to its input's.  `out` is a tensor, or a
     (q, k) pair of tensors, to write to; an output may be its own input.  Returns q's rotation,
     or the pair."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be a [B, Hq, N, d] tensor")
-    B, Hq, N, d = q.shape
-    dt, dev = _dtype_code(q), q.device
-    _check_operand("q", q, q.shape, q.dtype, dev)
-    _check_device(q)
-    xs = [q]
-    if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != 4:
-            raise ValueError("k must be a [B, Hk, N, d] tensor")
-        _check_operand("k", k, (B, k.shape[1], N, d), q.dtype, dev)
-        xs.append(k)
-    if (grid is None) == (positions is None):
-        raise ValueError("give either grid or positions")
-    pos_ptr, shared = None, 0
-    if positions is not None:
-        if (not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or positions.device != dev
-                or not positions.is_contiguous() or tuple(positions.shape) not in ((B, N, 3), (N, 3))):
-            raise ValueError(f"positions must be a contiguous int32 [{B}, {N}, 3] or [{N}, 3] tensor on {dev}")
-        pos_ptr, shared = positions.data_ptr(), int(positions.dim() == 2)
-    g = _geom(*(grid if grid is not None else (0, 1, 1)), 1, rope_split, theta, 0.0)
-    made = []
-    if out is None:
-        made = outs = [torch.empty(x.shape, dtype=x.dtype, device=dev) for x in xs]
-    else:
-        outs = list(out) if isinstance(out, (tuple, list)) else [out]
-        if len(outs) != len(xs):
-            raise ValueError(f"out must hold {len(xs)} tensors")
-        for i, (o, x) in enumerate(zip(outs, xs)):
-            _check_out(o, x.shape, x.dtype, dev)
-            in_place = o.data_ptr() == x.data_ptr() and o.stride() == x.stride()
-            _check_no_overlap(o, *(y for j, y in enumerate(xs) if j != i or not in_place), *outs[:i])
-    lay = None
-    if not all(t.is_contiguous() for t in (*xs, *outs)):
-        x, o = xs[-1], outs[-1]
-        lay = ctypes.byref(RopeLayouts(_layout(q), _layout(outs[0]), _layout(x), _layout(o)))
-    _check(lib.blin_rope(q.data_ptr(), outs[0].data_ptr(), Hq, None if k is None else k.data_ptr(),
-                         None if k is None else outs[1].data_ptr(), 0 if k is None else k.shape[1], dt, B, N, d,
-                         ctypes.byref(g), t0, pos_ptr, shared, 1 if inverse else 0, lay, _on_stream(stream, *made)))
-    return outs[0] if k is None else (outs[0], outs[1])
+    return _result(_ext.rope(q, k, rope_split, grid, t0, positions, theta, inverse, out, _handle(stream)))

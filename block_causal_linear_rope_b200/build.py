@@ -1,4 +1,4 @@
-"""Build libblin.so (C ABI + sm_100a kernels) in place with nvcc.
+"""Build libblin.so (C ABI + sm_100a kernels) with nvcc and its tensor-side extension with g++, in place.
 
     python block_causal_linear_rope_b200/build.py [--force] [--verbose-ptxas]
 
@@ -16,6 +16,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libblin.so")
+EXT = os.path.join(PKG, "_blin_torch.so")  # tensor-side marshalling (links libblin.so and torch)
+EXT_SRC = os.path.join(CSRC, "blin_torch.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 SOURCES = ["blin_api.cu", "blin_kernels.cu", "blin_noalloc.cu", "blin_tconv.cu", "blin_decay.cu",
@@ -33,6 +35,28 @@ def _inputs():
             [os.path.join(ROOT, "include", "blin.h")])
 
 
+def build_ext(force: bool = False) -> str:
+    """The CPython extension that checks tensors and calls the library."""
+    srcs = [EXT_SRC, os.path.join(ROOT, "include", "blin.h")]
+    if not force and os.path.exists(EXT) and all(os.path.getmtime(p) <= os.path.getmtime(EXT) for p in srcs):
+        return EXT
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    tmp = EXT + f".tmp{os.getpid()}"
+    lib = os.path.join(base, "lib")
+    subprocess.check_call([
+        os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wno-attributes",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in inc], EXT_SRC, "-o", tmp,
+        f"-L{PKG}", "-l:libblin.so", f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+        "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"])
+    os.replace(tmp, EXT)
+    return EXT
+
+
 def needs_build() -> bool:
     if not os.path.exists(LIB):
         return True
@@ -42,6 +66,7 @@ def needs_build() -> bool:
 
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if not force and not needs_build():
+        build_ext()
         return LIB
     objs = []
     for src in SOURCES:
@@ -55,6 +80,7 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([NVCC, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    build_ext(force)
     return LIB
 
 
