@@ -1,10 +1,11 @@
 // Rotary embedding over the axes (t, y, x), forward and inverse, of q and k in
 // one launch: pairs (2j, 2j+1) of each axis section turn by p * theta^(-2j/d_axis).
 //
-// Bound: HBM (each element read and written once, 3 flops each).  A CTA takes a
-// run of tokens and a run of heads: the (cos, sin) of its tokens are computed
-// once into shared memory and serve all its heads, so an angle costs one
-// evaluation per token and pair instead of one per head.
+// Bound: HBM (each element read and written once, 3 flops each).  A thread owns
+// one 16-byte piece of a token's row, computes the angles of its pairs once into
+// registers, and walks the heads with them: an angle costs one evaluation per
+// token and pair and CTA instead of one per head, and the loads of several heads
+// are in flight at a time.
 //
 // Angles: the frequency of a pair, in turns per position, is computed on the
 // host in double precision and handed over as a kernel argument; position x
@@ -26,6 +27,7 @@ using blin::Layout;
 
 constexpr int kMaxPairs = 128;
 constexpr int kThreads = 256;
+constexpr long long kCtas = 16 * 148;  // two rounds of eight CTAs on every SM
 
 struct RopeArgs {
     const void *in[2];
@@ -33,7 +35,7 @@ struct RopeArgs {
     Layout li[2], lo[2];
     int heads[2];         // q's and k's
     int B, N, d;
-    int tile;             // tokens per CTA
+    int tile, side;       // tokens per CTA, and heads it takes at a time
     int hsplit;           // CTAs that share a run of tokens, by heads
     int pairs, py, px;    // rotated pairs; first pair of the y and x sections
     int HW, Wg, t0;       // grid positions
@@ -67,53 +69,66 @@ __device__ __forceinline__ uint32_t rotate_bf16(uint32_t w, float2 cs) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-    constexpr int VN = 16 / (int)sizeof(T), VP = VN / 2;  // elements and pairs of a 16-byte piece
-    extern __shared__ float2 tab[];                        // [tile][pairs of whole pieces]
-    const int vecs = a.d / VN;                             // pieces per row
-    const int tp = (a.pairs + VP - 1) / VP * VP;           // table pairs per token
-    const int tiles = (a.N + a.tile - 1) / a.tile;
-    const int hs = blockIdx.x % a.hsplit;
-    const int bt = blockIdx.x / a.hsplit;
-    const int b = bt / tiles, n0 = (bt - b * tiles) * a.tile;
-    const int rows = min(a.tile, a.N - n0);
-    for (int i = threadIdx.x; i < rows * tp; i += kThreads) {
-        const int r = i / tp, p = i - r * tp;
-        tab[i] = p < a.pairs ? turn(a, b, n0 + r, p) : make_float2(1.f, 0.f);
-    }
-    __syncthreads();
-    const int all = a.heads[0] + a.heads[1];
-    const int h0 = (int)((long long)all * hs / a.hsplit), h1 = (int)((long long)all * (hs + 1) / a.hsplit);
-    const int per_head = rows * vecs;
-    for (int i = threadIdx.x; i < (h1 - h0) * per_head; i += kThreads) {
-        const int hh = i / per_head, e = i - hh * per_head, r = e / vecs, j = e - r * vecs;
-        int h = h0 + hh;
-        const int w = h >= a.heads[0];
-        h -= w ? a.heads[0] : 0;
-        const long long from = b * a.li[w].batch + h * a.li[w].head + (long long)(n0 + r) * a.li[w].tok + j * VN;
-        const long long to = b * a.lo[w].batch + h * a.lo[w].head + (long long)(n0 + r) * a.lo[w].tok + j * VN;
-        uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.in[w]) + from);
-        if (j * VP < a.pairs) {
-            const float2 *cs = tab + r * tp + j * VP;
-            if constexpr (sizeof(T) == 2) {
-                // a piece that straddles the last section's end: pairs past it are copied bit for bit
-                const int left = a.pairs - j * VP;
-                v.x = rotate_bf16(v.x, cs[0]);
-                if (left > 1) v.y = rotate_bf16(v.y, cs[1]);
-                if (left > 2) v.z = rotate_bf16(v.z, cs[2]);
-                if (left > 3) v.w = rotate_bf16(v.w, cs[3]);
-            } else {
-                float x = __uint_as_float(v.x), y = __uint_as_float(v.y);
+struct Piece {
+    static constexpr int VN = 16 / (int)sizeof(T), VP = VN / 2;  // elements and pairs
+    float2 cs[VP];
+    int left;  // pairs to rotate; those past the last section's end are copied bit for bit
+    __device__ __forceinline__ uint4 rotate(uint4 v) const {
+        if constexpr (sizeof(T) == 2) {
+            if (left > 0) v.x = rotate_bf16(v.x, cs[0]);
+            if (left > 1) v.y = rotate_bf16(v.y, cs[1]);
+            if (left > 2) v.z = rotate_bf16(v.z, cs[2]);
+            if (left > 3) v.w = rotate_bf16(v.w, cs[3]);
+        } else {
+            const float x = __uint_as_float(v.x), y = __uint_as_float(v.y), z = __uint_as_float(v.z), w = __uint_as_float(v.w);
+            if (left > 0) {
                 v.x = __float_as_uint(fmaf(x, cs[0].x, -y * cs[0].y));
                 v.y = __float_as_uint(fmaf(x, cs[0].y, y * cs[0].x));
-                if (a.pairs - j * VP > 1) {
-                    x = __uint_as_float(v.z), y = __uint_as_float(v.w);
-                    v.z = __float_as_uint(fmaf(x, cs[1].x, -y * cs[1].y));
-                    v.w = __float_as_uint(fmaf(x, cs[1].y, y * cs[1].x));
-                }
+            }
+            if (left > 1) {
+                v.z = __float_as_uint(fmaf(z, cs[1].x, -w * cs[1].y));
+                v.w = __float_as_uint(fmaf(z, cs[1].y, w * cs[1].x));
             }
         }
-        *reinterpret_cast<uint4 *>(static_cast<T *>(a.out[w]) + to) = v;
+        return v;
+    }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+    using P = Piece<T>;
+    constexpr int U = 4;  // heads in flight per thread
+    const int vecs = a.d / P::VN, per = a.tile * vecs;
+    const int tiles = (a.N + a.tile - 1) / a.tile;
+    const int hs = blockIdx.x % a.hsplit, bt = blockIdx.x / a.hsplit;
+    const int b = bt / tiles;
+    const int hh = threadIdx.x / per, e = threadIdx.x - hh * per, r = e / vecs, j = e - r * vecs;
+    const int n = (bt - b * tiles) * a.tile + r;
+    if (hh >= a.side || n >= a.N) return;
+    P piece;
+    piece.left = a.pairs - j * P::VP;
+#pragma unroll
+    for (int i = 0; i < P::VP; ++i)
+        piece.cs[i] = i < piece.left ? turn(a, b, n, j * P::VP + i) : make_float2(1.f, 0.f);
+    const int all = a.heads[0] + a.heads[1];
+    const int h0 = (int)((long long)all * hs / a.hsplit), h1 = (int)((long long)all * (hs + 1) / a.hsplit);
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {
+        const int first = w ? a.heads[0] : 0;
+        int h = max(h0 - first, 0) + hh;
+        const int end = min(h1 - first, a.heads[w]);
+        const T *in = static_cast<const T *>(a.in[w]) + b * a.li[w].batch + n * a.li[w].tok + j * P::VN;
+        T *out = static_cast<T *>(a.out[w]) + b * a.lo[w].batch + n * a.lo[w].tok + j * P::VN;
+        const long long si = a.li[w].head, so = a.lo[w].head;
+        for (; h < end; h += U * a.side) {
+            uint4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (h + u * a.side < end) v[u] = *reinterpret_cast<const uint4 *>(in + (h + u * a.side) * si);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (h + u * a.side < end) *reinterpret_cast<uint4 *>(out + (h + u * a.side) * so) = piece.rotate(v[u]);
+        }
     }
 }
 
@@ -194,22 +209,18 @@ extern "C" blin_status blin_rope(const void *q, void *q_out, int Hq, const void 
     for (int ax = 0, p = 0; ax < 3; ++ax)
         for (int j = 0; j < g->rope_split[ax] / 2; ++j, ++p)
             a.freq[p] = std::pow((double)g->theta, -2.0 * j / g->rope_split[ax]) * 0.15915494309189533577;
-    // Runs of 32 tokens whose angles serve every head; shorter runs, then fewer heads
-    // per CTA, while the call has too few CTAs for two on every SM.
-    a.tile = 32;
-    auto ctas = [&] { return (long long)B * ((N + a.tile - 1) / a.tile); };
-    while (a.tile > 1 && ctas() < 2 * 148) a.tile /= 2;
-    a.hsplit = 1;
-    const int per_head = a.tile * (d * (dt == BLIN_BF16 ? 2 : 4) / 16);  // 16-byte pieces of a head's run
-    while (a.hsplit < all && (ctas() * a.hsplit < 2 * 148 || (long long)(all / a.hsplit) * per_head > (1 << 30))) a.hsplit *= 2;
-    a.hsplit = std::min(a.hsplit, all);
-    if (ctas() * a.hsplit >= (1LL << 31)) return failf(BLIN_ERR_SHAPE, "problem too large");
-    const int vp = dt == BLIN_BF16 ? 4 : 2;
-    const size_t smem = sizeof(float2) * a.tile * ((a.pairs + vp - 1) / vp * vp);
+    // As many tokens as fill a CTA with one head's pieces, and several heads side by side where the call has
+    // fewer; heads are split over CTAs until there are kCtas, or each has one round of loads.
+    const int vecs = d * (dt == BLIN_BF16 ? 2 : 4) / 16;
+    a.tile = std::max(1, std::min(kThreads / vecs, N));
+    a.side = std::min(all, kThreads / (a.tile * vecs));
+    const long long runs = (long long)B * ((N + a.tile - 1) / a.tile);
+    a.hsplit = (int)std::max(1LL, std::min<long long>((kCtas + runs - 1) / runs, all / (4 * a.side)));
+    if (runs * a.hsplit >= (1LL << 31)) return failf(BLIN_ERR_SHAPE, "problem too large");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)(ctas() * a.hsplit);
-    if (dt == BLIN_BF16) rope_kernel<__nv_bfloat16><<<grid, kThreads, smem, s>>>(a);
-    else rope_kernel<float><<<grid, kThreads, smem, s>>>(a);
+    const unsigned grid = (unsigned)(runs * a.hsplit);
+    if (dt == BLIN_BF16) rope_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
+    else rope_kernel<float><<<grid, kThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return failf(BLIN_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));
     blin::note_launch();
