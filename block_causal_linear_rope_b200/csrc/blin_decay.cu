@@ -83,7 +83,9 @@ cudaError_t launch_decay_tc(const DecayArgs &a, int d, cudaStream_t s) {
 
 template <int D, typename T>
 static cudaError_t step(const DecayArgs &a, cudaStream_t s) {
-    decay_step_kernel<D, T><<<(unsigned)((long long)a.B * a.H * (D / 32)), D, 0, s>>>(a);
+    using Cf = StepCfg<D>;
+    const long long units = (long long)a.B * a.H * Cf::PER;
+    decay_step_kernel<D, T><<<(unsigned)((units + Cf::UPB - 1) / Cf::UPB), Cf::THREADS, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) note_launch();
     return e;

@@ -27,7 +27,7 @@ using blin::Layout;
 
 constexpr int kMaxPairs = 128;
 constexpr int kThreads = 256;
-constexpr long long kCtas = 16 * 148;  // two rounds of eight CTAs on every SM
+constexpr long long kCtas = 8 * 148;  // eight on every SM
 
 struct RopeArgs {
     const void *in[2];
@@ -97,7 +97,7 @@ struct Piece {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
     using P = Piece<T>;
-    constexpr int U = 4;  // heads in flight per thread
+    constexpr int U = 8;  // heads in flight per thread
     const int vecs = a.d / P::VN, per = a.tile * vecs;
     const int tiles = (a.N + a.tile - 1) / a.tile;
     const int hs = blockIdx.x % a.hsplit, bt = blockIdx.x / a.hsplit;

@@ -279,66 +279,91 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
 }
 
 // ---------------------------------------------------------------------------- one token
-// 32 columns of one head's state per CTA, 8 rows of 4 columns per thread: the
-// whole piece is in flight at once, each element is read and written once, and
-// splitting by columns leaves nothing to add up between CTAs.  Bound: HBM (8 d^2
-// bytes per head).
+// decay_slot by each warp for itself.
+__device__ __forceinline__ int decay_slot_warp(const DecayArgs &a, int b, int s, int lane) {
+    if (a.slot_of == nullptr || s < 0) return s;
+    int twice = 0;
+    if (s < a.slots)
+        for (int i = lane; i < b; i += 32) twice |= __ldg(a.slot_of + i) == s;
+    twice = __any_sync(~0u, twice);
+    if (s < a.slots && !twice) return s;
+    if (lane == 0) atomicCAS(a.wd, 0, s >= a.slots ? WD_SLOT_RANGE : WD_SLOT_TWICE);
+    return -1;
+}
+
+// A unit is 32 columns of one head's state; a thread takes 8 rows of 4 of them,
+// so that the whole piece is in flight at once, and each element is read and
+// written once.  Splitting by columns leaves nothing to add up between CTAs; at
+// d = 128 whole rows in one CTA of 512 threads took 108 us where this takes 86
+// (128 rows of 32 heads).  Bound: HBM (8 d^2 bytes per head); that call moves
+// 537 MB at 6.2 TB/s.
+template <int D>
+struct StepCfg {
+    static constexpr int CX = 8, RG = D / 8, TPU = CX * RG;  // column and row groups, threads per unit
+    static constexpr int THREADS = 128, UPB = THREADS / TPU, PER = D / 32;  // units per CTA, per head
+};
 template <int D, typename T>
-__global__ void __launch_bounds__(D) decay_step_kernel(const DecayArgs a) {
-    constexpr int RG = D / 8;  // row groups: thread rows rg + RG * r
-    __shared__ float4 part[D / 32][8];
-    const int tid = threadIdx.x, cx = tid & 7, rg = tid >> 3;
-    const long long u = blockIdx.x;
-    const int bh = (int)(u / (D / 32)), cg = (int)(u - (long long)bh * (D / 32));
-    const int b = bh / a.H, h = bh - b * a.H;
-    const int c0 = 32 * cg + 4 * cx;
+__global__ void __launch_bounds__(StepCfg<D>::THREADS) decay_step_kernel(const DecayArgs a) {
+    using Cf = StepCfg<D>;
+    constexpr int CX = Cf::CX, RG = Cf::RG, WPU = Cf::TPU / 32;  // warps of a unit
+    __shared__ float4 part[Cf::THREADS / 32][CX];
+    const int tid = threadIdx.x % Cf::TPU, lane = threadIdx.x & 31, cx = tid % CX, rg = tid / CX;
+    const long long u = (long long)blockIdx.x * Cf::UPB + threadIdx.x / Cf::TPU;
+    const bool there = u < (long long)a.B * a.H * Cf::PER;
+    const int bh = there ? (int)(u / Cf::PER) : 0, b = bh / a.H, h = bh - b * a.H;
+    const int c0 = 32 * (int)(u % Cf::PER) + 4 * cx;
     // the state's loads go out before the check for repeated slots: an entry in range is safe to read
-    int s = a.slot_of ? __ldg(a.slot_of + b) : b;
+    int s = there ? a.slot_of ? __ldg(a.slot_of + b) : b : -1;
     const bool in = s >= 0 && s < a.slots;
     float *sp = a.S + ((size_t)(in ? s : 0) * a.H + h) * D * D + c0;
     float4 st[8];
     if (in)
 #pragma unroll
         for (int r = 0; r < 8; ++r) st[r] = *reinterpret_cast<const float4 *>(sp + (rg + RG * r) * D);
-    s = decay_slot(a, b);
-    T *op = static_cast<T *>(a.o) + b * a.lo.batch + h * a.lo.head + c0;
+    s = decay_slot_warp(a, b, s, lane);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     if (s >= 0) {
         const T *qp = static_cast<const T *>(a.q) + b * a.lq.batch + h * a.lq.head;
         const T *kp = static_cast<const T *>(a.k) + b * a.lk.batch + h * a.lk.head;
         const T *vp = static_cast<const T *>(a.v) + b * a.lv.batch + h * a.lv.head + c0;
         const DecayMul mul(decay_log(a.log_decay, h), 1.f);
-        float v[4];
+        float v[4], k[8], q[8];
 #pragma unroll
         for (int w = 0; w < 4; ++w) v[w] = static_cast<float>(vp[w]);
 #pragma unroll
+        for (int r = 0; r < 8; ++r) k[r] = static_cast<float>(kp[rg + RG * r]), q[r] = static_cast<float>(qp[rg + RG * r]);
+#pragma unroll
         for (int r = 0; r < 8; ++r) {
-            const int i = rg + RG * r;
-            const float k = static_cast<float>(kp[i]), q = static_cast<float>(qp[i]);
             float x[4] = {st[r].x, st[r].y, st[r].z, st[r].w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                x[w] = fmaf(k, v[w], mul(x[w]));
-                acc[w] = fmaf(q, x[w], acc[w]);
+                x[w] = fmaf(k[r], v[w], mul(x[w]));
+                acc[w] = fmaf(q[r], x[w], acc[w]);
             }
-            *reinterpret_cast<float4 *>(sp + i * D) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(sp + (rg + RG * r) * D) = make_float4(x[0], x[1], x[2], x[3]);
         }
     }
-    // row groups: the four of a warp, then the warps
+    // row groups: those of a warp, then the unit's warps
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        acc[w] += __shfl_xor_sync(~0u, acc[w], 8);
-        acc[w] += __shfl_xor_sync(~0u, acc[w], 16);
-    }
-    if ((tid & 31) < 8) part[tid >> 5][cx] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    __syncthreads();
-    if (tid < 8) {
-        float4 t = part[0][tid];
+    for (int o = CX; o < 32; o *= 2)
 #pragma unroll
-        for (int w = 1; w < D / 32; ++w) {
-            const float4 x = part[w][tid];
-            t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+        for (int w = 0; w < 4; ++w) acc[w] += __shfl_xor_sync(~0u, acc[w], o);
+    float4 t = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if constexpr (WPU > 1) {
+        if (lane < CX) part[threadIdx.x / 32][lane] = t;
+        __syncthreads();
+        if (rg == 0) {
+            const int w0 = threadIdx.x / Cf::TPU * WPU;
+            t = part[w0][cx];
+#pragma unroll
+            for (int w = 1; w < WPU; ++w) {
+                const float4 x = part[w0 + w][cx];
+                t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+            }
         }
+    }
+    if (rg == 0 && there) {
+        T *op = static_cast<T *>(a.o) + b * a.lo.batch + h * a.lo.head + c0;
         op[0] = static_cast<T>(a.scale * t.x);
         op[1] = static_cast<T>(a.scale * t.y);
         op[2] = static_cast<T>(a.scale * t.z);
