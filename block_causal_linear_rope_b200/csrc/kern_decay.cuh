@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
     const T *kp = static_cast<const T *>(a.k) + b * a.lk.batch + h * a.lk.head;
     const T *vp = static_cast<const T *>(a.v) + b * a.lv.batch + h * a.lv.head;
     T *op = static_cast<T *>(a.o) + b * a.lo.batch + h * a.lo.head;
-    const DecayMul whole(lg, (float)C);
+    const DecaySplit whole(lg, (float)C);
     for (int n0 = begin; n0 < end; n0 += C) {
         const int n = min(C, end - n0);  // tokens of this chunk
         __syncthreads();
@@ -157,29 +157,35 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
         if (!STATES) {
             // a warp's rows end at 8 warp + 7: columns past them are masked and skipped
             const int jmax = 8 * (tid >> 5) + 8;
+            float acc[4][4];
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                const int j = tx + 16 * jj;
-                if (16 * jj < jmax) {
-                    for (int c = 0; c < D; c += 4) {
+            for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) acc[ii][jj] = 0.f;
+#pragma unroll 2
+            for (int c = 0; c < D; c += 4) {
+                float qv[4][4];
+#pragma unroll
+                for (int ii = 0; ii < 4; ++ii) lds_vec<4>(sq + (4 * ty + ii) * P + c, qv[ii]);
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) {
+                    if (16 * jj < jmax) {
                         float kv[4];
-                        lds_vec<4>(sk + j * P + c, kv);
+                        lds_vec<4>(sk + (tx + 16 * jj) * P + c, kv);
 #pragma unroll
-                        for (int ii = 0; ii < 4; ++ii) {
-                            float qv[4];
-                            lds_vec<4>(sq + (4 * ty + ii) * P + c, qv);
+                        for (int ii = 0; ii < 4; ++ii)
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) acc[ii] = fmaf(qv[u], kv[u], acc[ii]);
-                        }
+                            for (int u = 0; u < 4; ++u) acc[ii][jj] = fmaf(qv[ii][u], kv[u], acc[ii][jj]);
                     }
                 }
+            }
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
                 for (int ii = 0; ii < 4; ++ii) {
-                    const int i = 4 * ty + ii;
-                    sp[i * PP + j] = j <= i ? acc[ii] * pw[i - j] : 0.f;
+                    const int i = 4 * ty + ii, j = tx + 16 * jj;
+                    sp[i * PP + j] = j <= i ? acc[ii][jj] * pw[i - j] : 0.f;
                 }
-            }
             __syncthreads();
             float out[4][W], in[4][W];
 #pragma unroll
@@ -227,33 +233,45 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
                 }
             }
         }
+        // the values, weighted by their distance to the chunk's end
+        __syncthreads();
+        for (int i = tid; i < n * (D / 4); i += 256) {
+            const int j = i / (D / 4);
+            float4 *x = reinterpret_cast<float4 *>(sv + j * P + 4 * (i - j * (D / 4)));
+            const float f = pw[n - 1 - j];
+            *x = make_float4(f * x->x, f * x->y, f * x->z, f * x->w);
+        }
+        __syncthreads();
         // state: the chunk's decay, then its tokens
-        const DecayMul mul = n == C ? whole : DecayMul(lg, (float)n);
+        DecaySplit g = whole;
+        if (n < C) g = DecaySplit(lg, (float)n);
+        float add[W][W];
 #pragma unroll
         for (int r = 0; r < W; ++r)
 #pragma unroll
-            for (int w = 0; w < W; ++w) st[r][w] = mul(st[r][w]);
+            for (int w = 0; w < W; ++w) add[r][w] = 0.f;
+#pragma unroll 4
         for (int j = 0; j < n; ++j) {
             float kv[W], vv[W];
+            lds_vec<W>(sk + j * P + ty * W, kv);
             if constexpr (W <= 4) {
-                lds_vec<W>(sk + j * P + ty * W, kv);
                 lds_vec<W>(sv + j * P + tx * W, vv);
             } else {
-                lds_vec<W>(sk + j * P + ty * W, kv);
                 float x[4];
                 lds_vec<4>(sv + j * P + 4 * tx, x);
                 vv[0] = x[0], vv[1] = x[1], vv[2] = x[2], vv[3] = x[3];
                 lds_vec<4>(sv + j * P + 64 + 4 * tx, x);
                 vv[4] = x[0], vv[5] = x[1], vv[6] = x[2], vv[7] = x[3];
             }
-            const float f = pw[n - 1 - j];
-#pragma unroll
-            for (int w = 0; w < W; ++w) vv[w] *= f;
 #pragma unroll
             for (int r = 0; r < W; ++r)
 #pragma unroll
-                for (int w = 0; w < W; ++w) st[r][w] = fmaf(kv[r], vv[w], st[r][w]);
+                for (int w = 0; w < W; ++w) add[r][w] = fmaf(kv[r], vv[w], add[r][w]);
         }
+#pragma unroll
+        for (int r = 0; r < W; ++r)
+#pragma unroll
+            for (int w = 0; w < W; ++w) st[r][w] = fmaf(st[r][w], g.hi, fmaf(st[r][w], g.lo, add[r][w]));
     }
     if (STATES) {
         float *dst = wsp + (size_t)(seg + 1) * D * D;
