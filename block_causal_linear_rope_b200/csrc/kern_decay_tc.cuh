@@ -42,15 +42,15 @@ struct DecayTc {
     static constexpr int SUB = C * ROWB, TILE = NAT * SUB;
     static constexpr uint32_t LAYOUT = D == 32 ? 4u : 2u;  // 64B / 128B swizzle
     static constexpr int TPC = STATES ? 2 : 3;             // tiles landed per chunk: V, K (, Q)
-    static constexpr int NSLOT = D == 128 ? 5 : 9;
+    static constexpr int NSLOT = D == 128 ? 4 : 9;
     // weighted values: items of IT tokens, three parts each, in a ring of NVB
-    static constexpr int IT = D == 128 ? 16 : 64, NIT = C / IT, NVB = 2;
+    static constexpr int IT = D == 128 ? 32 : 64, NIT = C / IT, NVB = 2;
     static constexpr int VSUB = IT * ROWB, VPART = NAT * VSUB, VITEM = 3 * VPART;
     static constexpr int SIMG = 2 * D * D, NSB = D == 128 ? 1 : 2;  // bf16 state images
     static constexpr int OSTG = STATES || D == 128 ? 0 : TILE;      // output staging (d = 128: in the chunk's Q slot)
     static constexpr int OFF_V = NSLOT * TILE, OFF_S = OFF_V + NVB * VITEM, OFF_O = OFF_S + (STATES ? 0 : NSB * SIMG);
     static constexpr int OFF_CTRL = OFF_O + OSTG;
-    static constexpr int NBAR = 2 * NSLOT + 2 * NVB + 12;
+    static constexpr int NBAR = 2 * NSLOT + 2 * NVB + 11;
     static constexpr int OFF_PW = OFF_CTRL + 512;  // g^n for n = 0 .. 128, then scale g^{31 - m} for m < 32
     static constexpr int BYTES = OFF_PW + 4 * (132 + 32) + 1024;
     static_assert(8 * NBAR <= 504, "barriers");
@@ -77,7 +77,7 @@ struct DecayTc {
     static constexpr int RL = D == 128 ? 64 : 72;
     static constexpr int RX = !RSPLIT ? 0 : D == 128 ? 56 : 64, RT = !RSPLIT ? 0 : D == 128 ? 48 : 56,
                          RU = !RSPLIT ? 0 : D == 128 ? 96 : 112, RZ = !RSPLIT ? 0 : D == 128 ? 64 : 80,
-                         RC = !RSPLIT ? 0 : 40;
+                         RC = !RSPLIT ? 0 : D == 128 ? 48 : 72;
     static_assert(XW * RX + TW * RT + UW * RU + ZW * RZ + 4 * RC <= THREADS / 32 * RL, "registers");
 };
 
@@ -102,13 +102,13 @@ struct DecayUnit {
 
     // Barriers: full/empty of the landing slots, ready/free of the weighted values, then one each.  A wait
     // names a completion by its parity, so none may run two completions ahead of a role that waits for it:
-    //   sready(c), qsdone(c)  two barriers in turn each where there are two state images: the states' chain
-    //              and the outputs' run up to an image apart;
+    //   sready(c), ofull(c)  two barriers in turn each: the states' chain and the outputs' run up to a chunk
+    //              apart;
     //   B_CLEAN    completes once, in a last chunk with rows past the prompt's end;
     //   all others are completed again only after what waits for them has passed.
-    enum { B_SFULL, B_PREADY, B_KVFULL, B_KVEMPTY, B_SREADY, B_QSDONE = B_SREADY + 2, B_OFULL = B_QSDONE + 2, B_OEMPTY, B_CLEAN, B_DRAIN };
+    enum { B_SFULL, B_PREADY, B_KVFULL, B_KVEMPTY, B_SREADY, B_OFULL = B_SREADY + 2, B_OEMPTY = B_OFULL + 2, B_CLEAN, B_DRAIN };
     __device__ uint32_t sready(int c) const { return one(B_SREADY + (c & 1)); }
-    __device__ uint32_t qsdone(int c) const { return one(B_QSDONE + (c & 1)); }
+    __device__ uint32_t ofull(int c) const { return one(B_OFULL + (c & 1)); }
     __device__ uint32_t bar(int i) const { return ptx::smem_u32(bars + i); }
     __device__ uint32_t full(int s) const { return bar(s); }
     __device__ uint32_t empty(int s) const { return bar(Cf::NSLOT + s); }
@@ -122,8 +122,8 @@ struct DecayUnit {
     __device__ static int tv(int c) { return Cf::TPC * c; }
     __device__ static int tk(int c) { return Cf::TPC * c + 1; }
     __device__ static int tq(int c) { return Cf::TPC * c + 2; }
-    // `count` of the RELEASE arrivals that free tile t's slot: 8 by the warps that read it (K: the scores' for
-    // their product), 1 with the completion of the products that read it
+    // `count` of the RELEASE arrivals that free tile t's slot: 8 by the warps that read it or saw the scores
+    // made of it, 1 by those that see its last product complete
     __device__ void release(int t, int count) const { ptx::mbar_arrive_n(empty(t % Cf::NSLOT), count); }
 
     __device__ void init_barriers() const {
@@ -142,9 +142,8 @@ struct DecayUnit {
         ptx::mbar_init(one(B_SREADY), Cf::UW);
         ptx::mbar_init(one(B_SREADY + 1), Cf::UW);
         ptx::mbar_init(one(B_CLEAN), Cf::TW);
-        ptx::mbar_init(one(B_QSDONE), 1);
-        ptx::mbar_init(one(B_QSDONE + 1), 1);
         ptx::mbar_init(one(B_OFULL), 1);
+        ptx::mbar_init(one(B_OFULL + 1), 1);
         ptx::mbar_init(one(B_OEMPTY), Cf::OW);
         ptx::mbar_init(one(B_DRAIN), STATES ? 1 : 2);
     }
@@ -181,14 +180,27 @@ struct DecayUnit {
     }
 
     // ------------------------------------------------------------ MMA issuers (one thread each)
-    // An operand's descriptor is a constant plus its address in 16-byte units.
-    __device__ static uint64_t kmajor(uint32_t addr) { return ptx::smem_desc(addr, 16, 8 * Cf::ROWB, Cf::LAYOUT); }
-    __device__ static uint64_t mnmajor(uint32_t addr, uint32_t atom) {
-        return ptx::smem_desc(addr, atom, 8 * Cf::ROWB, Cf::LAYOUT);
-    }
-    // 16 features further along a K-major tile
-    __device__ static uint64_t kstep(int kk) {
-        return static_cast<uint64_t>((kk / (Cf::AW / 16)) * (Cf::SUB / 16) + (kk % (Cf::AW / 16)) * 2);
+    // An operand's descriptor: the address in 16-byte units in the low word, its layout in the high one.  The
+    // thread that issues the products has few instructions to spare for each (a product of 128 x 128 x 16
+    // takes 64 cycles), so steps along an operand are additions of constants to the low word.
+    struct Operand {
+        uint32_t lo, hi;
+        __device__ Operand(uint32_t addr, uint32_t atom) {
+            const uint64_t d = ptx::smem_desc(addr, atom, 8 * Cf::ROWB, Cf::LAYOUT);
+            lo = static_cast<uint32_t>(d);
+            hi = static_cast<uint32_t>(d >> 32);
+        }
+        __device__ Operand(uint32_t l, uint32_t h, int) : lo(l), hi(h) {}
+        __device__ Operand operator+(uint32_t bytes) const { return Operand(lo + (bytes >> 4), hi, 0); }
+    };
+    __device__ static Operand kmajor(uint32_t addr) { return Operand(addr, 16); }
+    __device__ static Operand mnmajor(uint32_t addr, uint32_t atom) { return Operand(addr, atom); }
+    // 16 features along a K-major tile, 16 rows along an MN-major one: bytes
+    static constexpr uint32_t kstep(int kk) { return (kk / (Cf::AW / 16)) * Cf::SUB + (kk % (Cf::AW / 16)) * 32; }
+    static constexpr uint32_t rstep(int kk) { return kk * 16 * Cf::ROWB; }
+    template <uint32_t ID, bool ACC>
+    __device__ static void mma(uint32_t d, Operand x, Operand y) {
+        ptx::mma_bf16_ss(d, x.lo, x.hi, y.lo, y.hi, ID, ACC);
     }
     // scores and outputs
     __device__ void mma_outputs() const {
@@ -199,76 +211,66 @@ struct DecayUnit {
                 break;
             // a chunk with rows past the prompt's end: once those are cleared
             if (tokens(c) < Cf::C && !wait(one(B_CLEAN), 0, WD_DC_VALUE)) break;
-            const uint64_t qd = kmajor(ptx::smem_u32(slot(tq(c)))), kd = kmajor(ptx::smem_u32(slot(tk(c))));
+            const Operand qd = kmajor(ptx::smem_u32(slot(tq(c)))), kd = kmajor(ptx::smem_u32(slot(tk(c))));
             // the scores' columns were last read by the PV product that this thread issued before
             constexpr uint32_t IDS = ptx::idesc_bf16_f32(128, 128, 0, 0), IDO = ptx::idesc_bf16_f32(128, D, 0, 1);
+            mma<IDS, false>(tmem, qd, kd);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) ptx::mma_bf16_ss(tmem, qd + kstep(kk), kd + kstep(kk), IDS, kk > 0);
+            for (int kk = 1; kk < D / 16; ++kk) mma<IDS, true>(tmem, qd + kstep(kk), kd + kstep(kk));
             ptx::mma_commit(one(B_SFULL));
             if (!wait(sready(c), c >> 1, WD_DC_STATE) || (c > 0 && !wait(one(B_OEMPTY), c - 1, WD_DC_OUT))) break;
             ptx::tc_fence_after_sync();
-            const uint64_t sd = mnmajor(ptx::smem_u32(sbuf(c)), D * Cf::ROWB);
+            const Operand sd = mnmajor(ptx::smem_u32(sbuf(c)), D * Cf::ROWB);
+            mma<IDO, false>(tmem + Cf::T_OI, qd, sd);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                ptx::mma_bf16_ss(tmem + Cf::T_OI, qd + kstep(kk), sd + static_cast<uint64_t>(kk * Cf::ROWB), IDO, kk > 0);
-            if (Cf::ZW) ptx::mma_commit(qsdone(c));
+            for (int kk = 1; kk < D / 16; ++kk) mma<IDO, true>(tmem + Cf::T_OI, qd + kstep(kk), sd + rstep(kk));
             if (!wait(full(tv(c) % Cf::NSLOT), tv(c) / Cf::NSLOT, WD_DC_FULL) || !wait(one(B_PREADY), c, WD_DC_SCORE)) break;
             ptx::tc_fence_after_sync();
-            const uint64_t vd = mnmajor(ptx::smem_u32(slot(tv(c))), Cf::SUB);
+            const Operand vd = mnmajor(ptx::smem_u32(slot(tv(c))), Cf::SUB);
 #pragma unroll
-            for (int kk = 0; kk < Cf::C / 16; ++kk)
-                ptx::mma_bf16_ts(tmem + Cf::T_OA, tmem + 16 * kk, vd + static_cast<uint64_t>(kk * Cf::ROWB), IDO, kk > 0);
-            ptx::mma_commit(one(B_OFULL));
-            ptx::mma_commit(empty(tv(c) % Cf::NSLOT));
-            if (D == 128) {
-                release(tq(c), 1);  // and by the warps whose rows leave from it
-            } else {
-                release(tq(c), Cf::RELEASE - 1);
-                ptx::mma_commit(empty(tq(c) % Cf::NSLOT));
+            for (int kk = 0; kk < Cf::C / 16; ++kk) {
+                const Operand v = vd + rstep(kk);
+                ptx::mma_bf16_ts(tmem + Cf::T_OA, tmem + 16 * kk, v.lo, v.hi, IDO, kk > 0);
             }
+            ptx::mma_commit(ofull(c));
         }
         drain();
     }
     // state product, item by item
     __device__ void mma_states() const {
         const int nc = chunks();
-        for (int c = 0; c < nc; ++c) {
+        const Operand v0 = mnmajor(ptx::smem_u32(vbuf(0)), Cf::VSUB);
+        static_assert(Cf::NIT % Cf::NVB == 0, "an item's buffer is known at compile time");
+        bool ok = true;
+        for (int c = 0; c < nc && ok; ++c) {
             if (!wait(full(tk(c) % Cf::NSLOT), tk(c) / Cf::NSLOT, WD_DC_FULL)) break;
             if (c > 0 && !wait(one(B_KVEMPTY), c - 1, WD_DC_STATE)) break;
             if (tokens(c) < Cf::C && !wait(one(B_CLEAN), 0, WD_DC_VALUE)) break;
-            const uint64_t kd = mnmajor(ptx::smem_u32(slot(tk(c))), D == 128 ? Cf::SUB : 0);
-            bool ok = true;
-#pragma unroll 1
+            const Operand kd = mnmajor(ptx::smem_u32(slot(tk(c))), D == 128 ? Cf::SUB : 0);
+#pragma unroll
             for (int it = 0; it < Cf::NIT; ++it) {
-                const int i = c * Cf::NIT + it;
-                if (!(ok = wait(vready(i % Cf::NVB), i / Cf::NVB, WD_DC_VALUE))) break;
+                constexpr int NB = Cf::NVB;
+                if (!(ok = ok && wait(vready(it % NB), (c * Cf::NIT + it) / NB, WD_DC_VALUE))) break;
                 ptx::tc_fence_after_sync();
-                const uint64_t ad = kd + static_cast<uint64_t>(it * (Cf::IT / 16) * Cf::ROWB);
-                const uint64_t vd = mnmajor(ptx::smem_u32(vbuf(i)), Cf::VSUB);
 #pragma unroll
                 for (int kk = 0; kk < Cf::IT / 16; ++kk) {
-                    const uint64_t bo = static_cast<uint64_t>(kk * Cf::ROWB);
-                    const uint32_t acc = it > 0 || kk > 0;
+                    const Operand k = kd + rstep(it * (Cf::IT / 16) + kk), v = v0 + (it % NB * Cf::VITEM + rstep(kk));
                     constexpr uint32_t ID = ptx::idesc_bf16_f32(Cf::KVM, Cf::KVN * D, 1, 1), ID1 = ptx::idesc_bf16_f32(Cf::KVM, D, 1, 1);
                     if constexpr (Cf::KVN == 1) {  // small parts first
-#pragma unroll
-                        for (int part = 2; part >= 0; --part)
-                            ptx::mma_bf16_ss(tmem + Cf::T_KV, ad + bo, vd + part * (Cf::VPART / 16) + bo, ID1, acc | (part < 2));
+                        if (it == 0 && kk == 0) mma<ID1, false>(tmem + Cf::T_KV, k, v + 2 * Cf::VPART);
+                        else mma<ID1, true>(tmem + Cf::T_KV, k, v + 2 * Cf::VPART);
+                        mma<ID1, true>(tmem + Cf::T_KV, k, v + Cf::VPART);
+                        mma<ID1, true>(tmem + Cf::T_KV, k, v);
                     } else {
-                        ptx::mma_bf16_ss(tmem + Cf::T_KV, ad + bo, vd + bo, ID, acc);
-                        if constexpr (Cf::KVN == 2)
-                            ptx::mma_bf16_ss(tmem + Cf::T_KV + D, ad + bo, vd + 2 * (Cf::VPART / 16) + bo, ID1, 1u);
+                        if (it == 0 && kk == 0) mma<ID, false>(tmem + Cf::T_KV, k, v);
+                        else mma<ID, true>(tmem + Cf::T_KV, k, v);
+                        if constexpr (Cf::KVN == 2) mma<ID1, true>(tmem + Cf::T_KV + D, k, v + 2 * Cf::VPART);
                     }
                 }
-                ptx::mma_commit(vfree(i % Cf::NVB));
+                ptx::mma_commit(vfree(it % NB));
             }
             if (!ok) break;
             ptx::mma_commit(one(B_KVFULL));
-            ptx::mma_commit(empty(tk(c) % Cf::NSLOT));
-            if (STATES) {
-                release(tk(c), Cf::RELEASE - 1);
-                release(tv(c), 1);
-            }
         }
         drain();
     }
@@ -395,7 +397,7 @@ struct DecayUnit {
                 ptx::fence_proxy_async_smem();  // written for the MMA; V read before its slot is filled again
                 warp_arrive(vready(i % Cf::NVB), lane);
             }
-            if (lane == 0) release(tv(c), 8 / Cf::TW);
+            if (lane == 0) release(tv(c), STATES && tid == 0 && tg == 0 ? 8 / Cf::TW + 1 : 8 / Cf::TW);
         }
     }
     static constexpr int ROWP = Cf::ROWB / 16;  // 16-byte pieces of a row of one atom
@@ -410,9 +412,19 @@ struct DecayUnit {
     }
     __device__ static uint32_t upper(float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); }
     __device__ static float2 rest(float2 v) {
-        return make_float2(v.x - __uint_as_float(__float_as_uint(v.x) & 0xFFFF0000u),
-                           v.y - __uint_as_float(__float_as_uint(v.y) & 0xFFFF0000u));
+        return fma2(make_float2(__uint_as_float(__float_as_uint(v.x) & 0xFFFF0000u), __uint_as_float(__float_as_uint(v.y) & 0xFFFF0000u)),
+                    make_float2(-1.f, -1.f), v);
     }
+    // two multiply-adds in one instruction
+    __device__ static float2 fma2(float2 x, float2 y, float2 z) {
+        float2 r;
+        asm("{\n\t.reg .b64 p, q, s;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 s, {%6, %7};\n\t"
+            "fma.rn.f32x2 p, p, q, s;\n\tmov.b64 {%0, %1}, p;\n}\n"
+            : "=f"(r.x), "=f"(r.y)
+            : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+        return r;
+    }
+    __device__ static float2 pair(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
 
     // ------------------------------------------------------------ state warps
     // Elements of the state a thread holds.  d = 128: row f = 32 sub + lane, 64 columns from col0.  Else the
@@ -500,11 +512,14 @@ struct DecayUnit {
 #pragma unroll
             for (int p = 0; p < Cf::KVN; ++p) ptx::tmem_pin(x[p]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float t = __uint_as_float(x[Cf::KVN - 1][i]);
+            for (int i = 0; i < 8; i += 2) {
+                float2 t = pair(x[Cf::KVN - 1][i], x[Cf::KVN - 1][i + 1]);
 #pragma unroll
-                for (int p = Cf::KVN - 2; p >= 0; --p) t += __uint_as_float(x[p][i]);
-                st[i0 + i] = fmaf(st[i0 + i], g.hi, fmaf(st[i0 + i], g.lo, t));
+                for (int p = Cf::KVN - 2; p >= 0; --p) t = fma2(pair(x[p][i], x[p][i + 1]), make_float2(1.f, 1.f), t);
+                const float2 v = make_float2(st[i0 + i], st[i0 + i + 1]);
+                t = fma2(v, make_float2(g.hi, g.hi), fma2(v, make_float2(g.lo, g.lo), t));
+                st[i0 + i] = t.x;
+                st[i0 + i + 1] = t.y;
             }
         }
     }
@@ -531,12 +546,13 @@ struct DecayUnit {
             add_product(st, g, pc);
             ptx::tc_fence_before_sync();
             warp_arrive(one(B_KVEMPTY), lane);
+            if (uw == 0 && lane == 0) release(tk(c), STATES ? Cf::RELEASE : 1);
             if constexpr (!STATES) {
                 if (c + 1 < nc) {
-                    // the next chunk's image goes where that of chunk c + 1 - NSB was: multiplied by now (without
-                    // output warps this warp has seen that chunk's outputs)
+                    // the next chunk's image goes where that of chunk c + 1 - NSB was, once that has been
+                    // multiplied (without output warps this warp has waited for it before)
                     const int u = c + 1 - Cf::NSB;
-                    if (Cf::ZW && u >= 0 && !(ok = wait(qsdone(u), u >> 1, WD_DC_STATE))) break;
+                    if (Cf::ZW && u >= 0 && !(ok = wait(ofull(u), u >> 1, WD_DC_OUT))) break;
                     put_state(st, sbuf(c + 1), pc, lane);
                     warp_arrive(sready(c + 1), lane);
                 }
@@ -567,10 +583,13 @@ struct DecayUnit {
             if (D == 128) release(tq(c - 1), 8 / Cf::OW);
         }
         __syncwarp();
-        if (!wait(one(B_OFULL), c, WD_DC_OUT)) return false;
+        if (!wait(ofull(c), c >> 1, WD_DC_OUT)) return false;
+        if (sub == 0 && lane == 0) {  // the chunk's products are done
+            release(tv(c), 1);
+            release(tq(c), D == 128 ? 1 : Cf::RELEASE);  // d = 128: and by the warps whose rows leave from it
+        }
         ptx::tc_fence_after_sync();
         uint8_t *stg = (D == 128 ? slot(tq(c)) : base + Cf::OFF_O) + 32 * sub * Cf::ROWB;
-        const uint32_t keep = r < n ? ~0u : 0u;  // rows past the prompt's end are zeros
 #pragma unroll 1
         for (int j = 0; j < D / 8; j += 2) {
             uint32_t x[16], y[16], o[8];
@@ -580,9 +599,13 @@ struct DecayUnit {
             ptx::tmem_pin(x);
             ptx::tmem_pin(y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                o[i] = keep & pack_bf16x2(fmaf(go, __uint_as_float(y[2 * i]), __uint_as_float(x[2 * i])),
-                                          fmaf(go, __uint_as_float(y[2 * i + 1]), __uint_as_float(x[2 * i + 1])));
+            for (int i = 0; i < 8; ++i) {
+                const float2 v = fma2(make_float2(go, go), pair(y[2 * i], y[2 * i + 1]), pair(x[2 * i], x[2 * i + 1]));
+                o[i] = pack_bf16x2(v.x, v.y);
+            }
+            if (r >= n)  // rows past the prompt's end are zeros
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = 0u;
             uint8_t *dst = stg + (j / ROWP) * Cf::SUB;
             *reinterpret_cast<uint4 *>(dst + swz_chunk<Cf::AW>(lane, j % ROWP)) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4 *>(dst + swz_chunk<Cf::AW>(lane, j % ROWP + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
