@@ -540,13 +540,13 @@ struct DecayUnit {
         for (int c = 0; c < nc && ok; ++c) {
             const int n = tokens(c);
             if (!(ok = wait(one(B_KVFULL), c, WD_DC_STATE))) break;
+            if (uw == 0 && lane == 0) release(tk(c), STATES ? Cf::RELEASE : 1);
             ptx::tc_fence_after_sync();
             DecaySplit g = whole;
             if (n < Cf::C) g = DecaySplit(lg, (float)n);
             add_product(st, g, pc);
             ptx::tc_fence_before_sync();
             warp_arrive(one(B_KVEMPTY), lane);
-            if (uw == 0 && lane == 0) release(tk(c), STATES ? Cf::RELEASE : 1);
             if constexpr (!STATES) {
                 if (c + 1 < nc) {
                     // the next chunk's image goes where that of chunk c + 1 - NSB was, once that has been
