@@ -67,6 +67,7 @@ static cudaError_t tc(const DecayArgs &a, const DecayMaps &m, cudaStream_t s) {
     using CS = DecayTc<D, true>;
     using CO = DecayTc<D, false>;
     if (CO::RSPLIT && !has_registers<decay_tc_kernel<D, false>>(CO::RL)) return cudaErrorInvalidConfiguration;
+    if (CS::RSPLIT && !has_registers<decay_tc_kernel<D, true>>(CS::RL)) return cudaErrorInvalidConfiguration;
     return launch_prompt<decay_tc_kernel<D, true>, decay_tc_kernel<D, false>>(a, CS::THREADS, CS::BYTES, CO::THREADS,
                                                                              CO::BYTES, s, m);
 }

@@ -42,15 +42,16 @@ struct DecayTc {
     static constexpr int SUB = C * ROWB, TILE = NAT * SUB;
     static constexpr uint32_t LAYOUT = D == 32 ? 4u : 2u;  // 64B / 128B swizzle
     static constexpr int TPC = STATES ? 2 : 3;             // tiles landed per chunk: V, K (, Q)
-    static constexpr int NSLOT = D == 128 ? 4 : 9;
+    static constexpr int NSLOT = D != 128 ? 9 : STATES ? 4 : 5;
     // weighted values: items of IT tokens, three parts each, in a ring of NVB
-    static constexpr int IT = D == 128 ? 32 : 64, NIT = C / IT, NVB = 2;
+    static constexpr int IT = D == 128 ? 16 : D == 64 && STATES ? 32 : 64, NIT = C / IT;
+    static constexpr int NVB = !STATES ? 2 : D == 128 ? 8 : D == 64 ? 4 : 2;
     static constexpr int VSUB = IT * ROWB, VPART = NAT * VSUB, VITEM = 3 * VPART;
     static constexpr int SIMG = 2 * D * D, NSB = D == 128 ? 1 : 2;  // bf16 state images
     static constexpr int OSTG = STATES || D == 128 ? 0 : TILE;      // output staging (d = 128: in the chunk's Q slot)
     static constexpr int OFF_V = NSLOT * TILE, OFF_S = OFF_V + NVB * VITEM, OFF_O = OFF_S + (STATES ? 0 : NSB * SIMG);
     static constexpr int OFF_CTRL = OFF_O + OSTG;
-    static constexpr int NBAR = 2 * NSLOT + 2 * NVB + 11;
+    static constexpr int NBAR = 2 * NSLOT + 2 * NVB + 13;
     static constexpr int OFF_PW = OFF_CTRL + 512;  // g^n for n = 0 .. 128, then scale g^{31 - m} for m < 32
     static constexpr int BYTES = OFF_PW + 4 * (132 + 32) + 1024;
     static_assert(8 * NBAR <= 504, "barriers");
@@ -58,26 +59,28 @@ struct DecayTc {
     // Warps: XG and TG warpgroups share the scores and the values of a chunk, UW warps hold the state, ZW the
     // outputs (0: the state's do both).  A d = 32 CTA has one warpgroup of each and no ZW, as two CTAs share an
     // SM.  The last warpgroup holds the producer and the MMA threads.
-    static constexpr int XG = STATES ? 0 : D == 32 ? 1 : 2, TG = D == 32 ? 1 : 2, UW = D == 128 ? 8 : 4;
+    static constexpr int XG = STATES ? 0 : D == 32 ? 1 : 2, TG = STATES ? (D == 32 ? 2 : 4) : D == 32 ? 1 : 2,
+                         UW = D == 128 ? 8 : 4;
     static constexpr int XW = 4 * XG, TW = 4 * TG, ZW = STATES || D == 32 ? 0 : 4, OW = ZW ? ZW : UW;
     static constexpr int THREADS = 32 * (XW + TW + UW + ZW + 4);
-    static constexpr int RELEASE = 9;  // arrivals that free a landing slot
+    static constexpr int SHARE = 16, RELEASE = SHARE + 1;  // arrivals that free a landing slot
     // TMEM columns: scores / P, inner and carried outputs, state product.  The three parts of the values
     // multiply side by side where there is room for a column range each (KVN = 3), else the low part is
     // added to the middle one's (2), or all to one (1).
     static constexpr int KVN = D == 128 ? 1 : D == 64 || STATES ? 3 : 2, KVC = KVN * D;
+    static constexpr int KB = STATES ? 2 : 1;  // state products in TMEM
     static constexpr int KVM = D == 128 ? 128 : 64;  // rows of the state product
     static constexpr int T_OA = 128, T_OI = T_OA + D, T_KV = STATES ? 0 : T_OI + D;
-    static constexpr int TCOLS = STATES ? (D == 64 ? 256 : 128) : D == 32 ? 256 : 512;
-    static_assert(T_KV + KVC <= TCOLS, "TMEM columns");
+    static constexpr int TCOLS = D == 32 ? 256 : STATES && D == 128 ? 256 : 512;
+    static_assert(T_KV + KB * KVC <= TCOLS, "TMEM columns");
     static constexpr int NCOL = D == 128 ? 64 : D * D / 128;  // state columns per thread
-    // d >= 64: the kernel is launched with RL registers a thread, and the warpgroups that hold the state or
-    // the outputs draw on what the others give up
-    static constexpr bool RSPLIT = D != 32 && !STATES;
-    static constexpr int RL = D == 128 ? 64 : 72;
-    static constexpr int RX = !RSPLIT ? 0 : D == 128 ? 56 : 64, RT = !RSPLIT ? 0 : D == 128 ? 48 : 56,
-                         RU = !RSPLIT ? 0 : D == 128 ? 96 : 112, RZ = !RSPLIT ? 0 : D == 128 ? 64 : 80,
-                         RC = !RSPLIT ? 0 : D == 128 ? 48 : 72;
+    // With many warps the kernel is launched with RL registers a thread, and the warpgroups that hold the state
+    // or the outputs draw on what the others give up.
+    static constexpr bool RSPLIT = STATES ? D == 128 : D != 32;
+    static constexpr int RL = D == 128 && !STATES ? 64 : 72;
+    static constexpr int RX = !RSPLIT ? 0 : D == 128 ? 56 : 64, RT = !RSPLIT ? 0 : D == 128 && !STATES ? 48 : 56,
+                         RU = !RSPLIT ? 0 : D == 64 ? 112 : STATES ? 104 : 96, RZ = !RSPLIT ? 0 : D == 128 ? 64 : 80,
+                         RC = !RSPLIT ? 0 : D == 128 && !STATES ? 48 : STATES ? 56 : 72;
     static_assert(XW * RX + TW * RT + UW * RU + ZW * RZ + 4 * RC <= THREADS / 32 * RL, "registers");
 };
 
@@ -102,11 +105,13 @@ struct DecayUnit {
 
     // Barriers: full/empty of the landing slots, ready/free of the weighted values, then one each.  A wait
     // names a completion by its parity, so none may run two completions ahead of a role that waits for it:
-    //   sready(c), ofull(c)  two barriers in turn each: the states' chain and the outputs' run up to a chunk
-    //              apart;
+    //   sready(c), ofull(c), kvfull(c), kvempty(c)  two barriers in turn each: the states' chain and the
+    //              outputs', or two state products, run up to a chunk apart;
     //   B_CLEAN    completes once, in a last chunk with rows past the prompt's end;
     //   all others are completed again only after what waits for them has passed.
-    enum { B_SFULL, B_PREADY, B_KVFULL, B_KVEMPTY, B_SREADY, B_OFULL = B_SREADY + 2, B_OEMPTY = B_OFULL + 2, B_CLEAN, B_DRAIN };
+    enum { B_SFULL, B_PREADY, B_KVFULL, B_KVEMPTY = B_KVFULL + 2, B_SREADY = B_KVEMPTY + 2, B_OFULL = B_SREADY + 2, B_OEMPTY = B_OFULL + 2, B_CLEAN, B_DRAIN };
+    __device__ uint32_t kvfull(int c) const { return one(B_KVFULL + (c & 1)); }
+    __device__ uint32_t kvempty(int c) const { return one(B_KVEMPTY + (c & 1)); }
     __device__ uint32_t sready(int c) const { return one(B_SREADY + (c & 1)); }
     __device__ uint32_t ofull(int c) const { return one(B_OFULL + (c & 1)); }
     __device__ uint32_t bar(int i) const { return ptx::smem_u32(bars + i); }
@@ -122,7 +127,7 @@ struct DecayUnit {
     __device__ static int tv(int c) { return Cf::TPC * c; }
     __device__ static int tk(int c) { return Cf::TPC * c + 1; }
     __device__ static int tq(int c) { return Cf::TPC * c + 2; }
-    // `count` of the RELEASE arrivals that free tile t's slot: 8 by the warps that read it or saw the scores
+    // `count` of the RELEASE arrivals that free tile t's slot: SHARE by the warps that read it or saw the scores
     // made of it, 1 by those that see its last product complete
     __device__ void release(int t, int count) const { ptx::mbar_arrive_n(empty(t % Cf::NSLOT), count); }
 
@@ -136,15 +141,15 @@ struct DecayUnit {
             ptx::mbar_init(vfree(s), 1);
         }
         ptx::mbar_init(one(B_SFULL), 1);
-        ptx::mbar_init(one(B_PREADY), Cf::XW);
-        ptx::mbar_init(one(B_KVFULL), 1);
-        ptx::mbar_init(one(B_KVEMPTY), Cf::UW);
-        ptx::mbar_init(one(B_SREADY), Cf::UW);
-        ptx::mbar_init(one(B_SREADY + 1), Cf::UW);
-        ptx::mbar_init(one(B_CLEAN), Cf::TW);
-        ptx::mbar_init(one(B_OFULL), 1);
-        ptx::mbar_init(one(B_OFULL + 1), 1);
+        ptx::mbar_init(one(B_PREADY), STATES ? 1 : Cf::XW);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(one(B_KVFULL + i), 1);
+            ptx::mbar_init(one(B_KVEMPTY + i), Cf::UW);
+            ptx::mbar_init(one(B_SREADY + i), Cf::UW);
+            ptx::mbar_init(one(B_OFULL + i), 1);
+        }
         ptx::mbar_init(one(B_OEMPTY), Cf::OW);
+        ptx::mbar_init(one(B_CLEAN), Cf::TW);
         ptx::mbar_init(one(B_DRAIN), STATES ? 1 : 2);
     }
     // Waits for completion number `k` (from 0) of a barrier; false: gave up.  A role that gives up stops,
@@ -244,7 +249,8 @@ struct DecayUnit {
         bool ok = true;
         for (int c = 0; c < nc && ok; ++c) {
             if (!wait(full(tk(c) % Cf::NSLOT), tk(c) / Cf::NSLOT, WD_DC_FULL)) break;
-            if (c > 0 && !wait(one(B_KVEMPTY), c - 1, WD_DC_STATE)) break;
+            if (c >= Cf::KB && !wait(kvempty(c - Cf::KB), (c - Cf::KB) >> 1, WD_DC_STATE)) break;
+            const uint32_t to = tmem + Cf::T_KV + c % Cf::KB * Cf::KVC;
             if (tokens(c) < Cf::C && !wait(one(B_CLEAN), 0, WD_DC_VALUE)) break;
             const Operand kd = mnmajor(ptx::smem_u32(slot(tk(c))), D == 128 ? Cf::SUB : 0);
 #pragma unroll
@@ -257,20 +263,20 @@ struct DecayUnit {
                     const Operand k = kd + rstep(it * (Cf::IT / 16) + kk), v = v0 + (it % NB * Cf::VITEM + rstep(kk));
                     constexpr uint32_t ID = ptx::idesc_bf16_f32(Cf::KVM, Cf::KVN * D, 1, 1), ID1 = ptx::idesc_bf16_f32(Cf::KVM, D, 1, 1);
                     if constexpr (Cf::KVN == 1) {  // small parts first
-                        if (it == 0 && kk == 0) mma<ID1, false>(tmem + Cf::T_KV, k, v + 2 * Cf::VPART);
-                        else mma<ID1, true>(tmem + Cf::T_KV, k, v + 2 * Cf::VPART);
-                        mma<ID1, true>(tmem + Cf::T_KV, k, v + Cf::VPART);
-                        mma<ID1, true>(tmem + Cf::T_KV, k, v);
+                        if (it == 0 && kk == 0) mma<ID1, false>(to, k, v + 2 * Cf::VPART);
+                        else mma<ID1, true>(to, k, v + 2 * Cf::VPART);
+                        mma<ID1, true>(to, k, v + Cf::VPART);
+                        mma<ID1, true>(to, k, v);
                     } else {
-                        if (it == 0 && kk == 0) mma<ID, false>(tmem + Cf::T_KV, k, v);
-                        else mma<ID, true>(tmem + Cf::T_KV, k, v);
-                        if constexpr (Cf::KVN == 2) mma<ID1, true>(tmem + Cf::T_KV + D, k, v + 2 * Cf::VPART);
+                        if (it == 0 && kk == 0) mma<ID, false>(to, k, v);
+                        else mma<ID, true>(to, k, v);
+                        if constexpr (Cf::KVN == 2) mma<ID1, true>(to + D, k, v + 2 * Cf::VPART);
                     }
                 }
                 ptx::mma_commit(vfree(it % NB));
             }
             if (!ok) break;
-            ptx::mma_commit(one(B_KVFULL));
+            ptx::mma_commit(kvfull(c));
         }
         drain();
     }
@@ -295,7 +301,7 @@ struct DecayUnit {
         const int nc = chunks();
         for (int c = 0; c < nc; ++c) {
             if (!wait(one(B_SFULL), c, WD_DC_SCORE)) break;
-            if (xw == 0 && lane == 0) release(tk(c), Cf::RELEASE - 1);  // multiplied by the queries
+            if (xw == 0 && lane == 0) release(tk(c), Cf::SHARE);  // multiplied by the queries
             ptx::tc_fence_after_sync();
 #pragma unroll 1
             for (int g = x0; g < 2 * w; g += XG) {
@@ -351,6 +357,7 @@ struct DecayUnit {
     // turn.
     __device__ void values(int tid, int lane) const {
         constexpr int PARTS = 128 / Cf::IT, PCS = D / 8 / PARTS;
+        static_assert(PCS >= 1, "a thread has a piece to write");
         const int tg = tid >> 7;
         tid &= 127;
         const int r = tid % Cf::IT, part = tid / Cf::IT;
@@ -397,7 +404,7 @@ struct DecayUnit {
                 ptx::fence_proxy_async_smem();  // written for the MMA; V read before its slot is filled again
                 warp_arrive(vready(i % Cf::NVB), lane);
             }
-            if (lane == 0) release(tv(c), STATES && tid == 0 && tg == 0 ? 8 / Cf::TW + 1 : 8 / Cf::TW);
+            if (lane == 0) release(tv(c), Cf::SHARE / Cf::TW + (STATES && tid == 0 && tg == 0 ? 1 : 0));
         }
     }
     static constexpr int ROWP = Cf::ROWB / 16;  // 16-byte pieces of a row of one atom
@@ -497,14 +504,14 @@ struct DecayUnit {
         ptx::fence_proxy_async_smem();
     }
     // S <- g S + this chunk's product
-    __device__ void add_product(float (&st)[Cf::NCOL], const DecaySplit &g, const Piece &pc) const {
+    __device__ void add_product(float (&st)[Cf::NCOL], const DecaySplit &g, const Piece &pc, int c) const {
 #pragma unroll
         for (int i0 = 0; i0 < Cf::NCOL; i0 += 8) {
             uint32_t x[Cf::KVN][8];
             const int col = D == 128 ? i0 : 2 * i0;  // 8 columns of a row, or 16 columns of two half rows
 #pragma unroll
             for (int p = 0; p < Cf::KVN; ++p) {
-                const uint32_t at = pc.row + Cf::T_KV + p * D + pc.col0 + col;
+                const uint32_t at = pc.row + Cf::T_KV + c % Cf::KB * Cf::KVC + p * D + pc.col0 + col;
                 if constexpr (D == 128) ptx::tmem_ld(at, x[p]);
                 else ptx::tmem_ld_16x256(at, x[p]);
             }
@@ -539,14 +546,14 @@ struct DecayUnit {
         bool ok = true;
         for (int c = 0; c < nc && ok; ++c) {
             const int n = tokens(c);
-            if (!(ok = wait(one(B_KVFULL), c, WD_DC_STATE))) break;
+            if (!(ok = wait(kvfull(c), c >> 1, WD_DC_STATE))) break;
             if (uw == 0 && lane == 0) release(tk(c), STATES ? Cf::RELEASE : 1);
             ptx::tc_fence_after_sync();
             DecaySplit g = whole;
             if (n < Cf::C) g = DecaySplit(lg, (float)n);
-            add_product(st, g, pc);
+            add_product(st, g, pc, c);
             ptx::tc_fence_before_sync();
-            warp_arrive(one(B_KVEMPTY), lane);
+            warp_arrive(kvempty(c), lane);
             if constexpr (!STATES) {
                 if (c + 1 < nc) {
                     // the next chunk's image goes where that of chunk c + 1 - NSB was, once that has been
@@ -580,7 +587,7 @@ struct DecayUnit {
         const uint32_t row = tmem + (static_cast<uint32_t>(32 * sub) << 16);
         if (lane == 0 && c > 0) {  // the staged rows of the last chunk have left
             ptx::bulk_wait_group_read<0>();
-            if (D == 128) release(tq(c - 1), 8 / Cf::OW);
+            if (D == 128) release(tq(c - 1), Cf::SHARE / Cf::OW);
         }
         __syncwarp();
         if (!wait(ofull(c), c >> 1, WD_DC_OUT)) return false;
