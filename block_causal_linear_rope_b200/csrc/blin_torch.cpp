@@ -215,6 +215,7 @@ PyObject *decay_prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t N = c.q.size(2);
         const int *lengths = static_cast<const int *>(optional(a[6], "lengths", at::kInt, {c.B}, c.q));
         const Tensor out = c.output(a[8]);
+        if (N == 0 && c.B > 0 && c.H > 0) return THPVariable_Wrap(out);  // no tokens: nothing to read, no address to give
         const size_t need = blin_decay_workspace_size((int)c.B, (int)c.H, (int)N, (int)c.d, c.dt);
         Tensor scratch;
         void *ws = nullptr;
@@ -305,6 +306,15 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
             if (two) no_overlap(out[0], out[1]);
         }
         if (!two) out[1] = out[0];
+        auto result = [&]() -> PyObject * {
+            if (!two) return THPVariable_Wrap(out[0]);
+            PyObject *x = THPVariable_Wrap(out[0]), *y = THPVariable_Wrap(out[1]);
+            PyObject *both = x && y ? PyTuple_Pack(2, x, y) : nullptr;
+            Py_XDECREF(x);
+            Py_XDECREF(y);
+            return both;
+        };
+        if (N == 0 && B > 0 && q.size(1) > 0 && k.size(1) > 0) return result();
         const cudaStream_t s = stream_of(a[9], q, {&made[0], &made[1]});
         const bool dense = q.is_contiguous() && k.is_contiguous() && out[0].is_contiguous() && out[1].is_contiguous();
         const blin_rope_layouts lay{layout(q), layout(out[0]), layout(k), layout(out[1])};
@@ -312,13 +322,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
             blin_rope(q.const_data_ptr(), out[0].data_ptr(), (int)q.size(1), two ? k.const_data_ptr() : nullptr,
                       two ? out[1].data_ptr() : nullptr, two ? (int)k.size(1) : 0, dt, (int)B, (int)N, (int)d, &g,
                       (int)integer(a[4], "t0"), pos, shared, inverse, dense ? nullptr : &lay, s);
-        if (rc != BLIN_OK) return PyLong_FromLong(rc);
-        if (!two) return THPVariable_Wrap(out[0]);
-        PyObject *x = THPVariable_Wrap(out[0]), *y = THPVariable_Wrap(out[1]);
-        PyObject *pair = x && y ? PyTuple_Pack(2, x, y) : nullptr;
-        Py_XDECREF(x);
-        Py_XDECREF(y);
-        return pair;
+        return rc == BLIN_OK ? result() : PyLong_FromLong(rc);
     });
 }
 

@@ -279,3 +279,51 @@ def test_the_binding_refuses(blin):
             blin.decay_step(x, k[:, :, 0], v[:, :, 0], lg, pool, **kw)
     with pytest.raises(blin.BlinError, match="ALIGN"):
         blin.decay_prefill(*(torch.zeros(1, 1, 8, 68, dtype=torch.bfloat16, device="cuda")[..., 4:] for _ in range(3)), lg[:1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_no_tokens(blin, dtype):
+    q = torch.empty(2, 3, 0, 64, dtype=DT[dtype], device="cuda")
+    pool = torch.ones(2, 3, 64, 64, device="cuda")
+    assert blin.decay_prefill(q, q, q, torch.zeros(3, device="cuda"), state=pool).shape == q.shape
+    assert (pool == 1).all()
+    qr, kr = blin.rope(q, q, grid=(0, 2, 2), rope_split=(16, 24, 24))
+    assert qr.shape == kr.shape == q.shape
+
+
+def test_rope_prompt_and_steps_together(blin):
+    """As a service runs them: q and k of a fused projection rotated in place over a latent grid, the
+    prompt into pool slots, then a single token at a time with given positions; against the oracle
+    over the whole sequence.  Each rotated value is off by at most 2^-20 of its pair's length, which
+    is at most the sum of the pair's absolute values: 2^-18 A covers both operands of a product."""
+    B, H, d, split, grid, extra = 2, 3, 64, (16, 24, 16), (3, 4, 5), 4
+    N = grid[0] * grid[1] * grid[2]
+    rng = np.random.default_rng(12)
+    qkv = rng.standard_normal((B, N + extra, 3, H, d)).astype(np.float32)
+    lg = torch.tensor([-0.03, -0.4, 0.0], device="cuda")
+    pool = torch.zeros(4, H, d, d, device="cuda")
+    slots = torch.tensor([3, 1], dtype=torch.int32, device="cuda")
+    fused = torch.from_numpy(qkv[:, :N].copy()).cuda()
+    q, k, v = (fused[:, :, i].transpose(1, 2) for i in range(3))
+    blin.rope(q, k, grid=grid, t0=2, rope_split=split, out=(q, k))
+    outs = [blin.decay_prefill(q, k, v, lg, state=pool, slots=slots, scale=d ** -0.5)]
+    pos = list(od.rope_positions(*grid, t0=2))
+    for n in range(N, N + extra):
+        at = torch.tensor([[n, n, n]], dtype=torch.int32, device="cuda")  # text behind the video
+        pos.append(np.array([n, n, n]))
+        row = torch.from_numpy(qkv[:, n].copy()).cuda()  # [B, 3, H, d]
+        q1, k1 = blin.rope(row[:, 0].unsqueeze(2), row[:, 1].unsqueeze(2), positions=at, rope_split=split)
+        outs.append(blin.decay_step(q1.squeeze(2), k1.squeeze(2), row[:, 2], lg, pool, slots=slots,
+                                    scale=d ** -0.5).unsqueeze(2))
+    x = qkv.transpose(2, 0, 3, 1, 4).astype(np.float64)
+    qr, kr = (od.rope(t, np.array(pos), split) for t in x[:2])
+    want, S = od.decay_attention(qr, kr, x[2], f64(lg), d ** -0.5)
+
+    def lengths(t):  # each feature's bound: its pair's absolute sum
+        y = abs(t).reshape(*t.shape[:-1], -1, 2)
+        return (y.sum(-1, keepdims=True) + 0 * y).reshape(t.shape)
+
+    A, SA = od.decay_attention(lengths(x[0]), lengths(x[1]), abs(x[2]), f64(lg), d ** -0.5)
+    assert (abs(f64(torch.cat(outs, dim=2)) - want) <= (2.0 ** -18 + (d + 272) * 2.0 ** -24) * A).all()
+    got = f64(pool)
+    assert (abs(got[[3, 1]] - S) <= 2.0 ** -17 * SA).all() and not got[[0, 2]].any()
