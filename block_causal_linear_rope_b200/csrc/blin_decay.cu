@@ -40,7 +40,7 @@ static cudaError_t launch_prompt(const DecayArgs &a, int states_threads, int sta
 template <int D>
 static cudaError_t simt(const DecayArgs &a, cudaStream_t s) {
     constexpr int smem = SimtCfg<D>::BYTES;
-    return launch_prompt<decay_simt_kernel<D, float, true>, decay_simt_kernel<D, float, false>>(a, 256, smem, 256, smem, s);
+    return launch_prompt<decay_simt_kernel<D, true>, decay_simt_kernel<D, false>>(a, 256, smem, 256, smem, s);
 }
 
 cudaError_t launch_decay_simt(const DecayArgs &a, int d, cudaStream_t s) {

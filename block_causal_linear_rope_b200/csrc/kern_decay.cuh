@@ -6,42 +6,6 @@
 
 namespace blin {
 
-template <typename T>
-struct Vec16;  // 16 bytes of T widened to fp32
-template <>
-struct Vec16<float> {
-    static constexpr int N = 4;
-    __device__ __forceinline__ static void load(const float *p, float (&f)[4]) {
-        const float4 v = *reinterpret_cast<const float4 *>(p);
-        f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-    }
-    __device__ __forceinline__ static void store(float *p, const float (&f)[4]) {
-        *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    }
-};
-template <>
-struct Vec16<__nv_bfloat16> {
-    static constexpr int N = 8;
-    __device__ __forceinline__ static void load(const __nv_bfloat16 *p, float (&f)[8]) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-    __device__ __forceinline__ static void store(__nv_bfloat16 *p, const float (&f)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
-
 // ---------------------------------------------------------------------------- prompts
 constexpr int kSimtChunk = 64;
 
@@ -49,37 +13,44 @@ template <int D>
 struct SimtCfg {
     static constexpr int C = kSimtChunk, P = D + 4;  // rows padded by 16 bytes: no bank conflicts on 16-byte reads
     static constexpr int PP = C + 4;
-    static constexpr int FLOATS = 3 * C * P + C * PP + D * P + 2 * C;
+    static constexpr int FLOATS = 4 * C * P + C * PP + D * P + C + 4;
     static constexpr int BYTES = FLOATS * 4;
 };
 
+// V consecutive floats of shared memory, 16 bytes at a time, the second 16 bytes `far` floats on.
 template <int V>
-__device__ __forceinline__ void lds_vec(const float *p, float (&f)[V]) {
+__device__ __forceinline__ void lds_vec(const float *p, int far, float (&f)[V]) {
     if constexpr (V == 2) {
         const float2 v = *reinterpret_cast<const float2 *>(p);
         f[0] = v.x, f[1] = v.y;
     } else {
 #pragma unroll
         for (int i = 0; i < V / 4; ++i) {
-            const float4 v = *reinterpret_cast<const float4 *>(p + 4 * i);
+            const float4 v = *reinterpret_cast<const float4 *>(p + far * i);
             f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
         }
     }
 }
 
-// One segment of one head, 64 tokens at a time:
+// One segment of one fp32 head, 64 tokens at a time:
 //   o_i = scale (sum_{j <= i} g^{i-j} (q_i . k_j) v_j + g^{i+1} q_i S),
-//   S  <- g^n S + sum_j g^{n-1-j} k_j^T v_j.
+//   S  <- g^n S + sum_j (g^{n-1-j} k_j)^T v_j.
 // 16 x 16 threads hold a 4 x 4 tile of the scores, 4 x D/16 of the outputs and
-// D/16 x D/16 of the state; the state's fp32 values stay in registers and a copy
-// in shared memory feeds the products.  STATES: local states only (phase 1).
-template <int D, typename T, bool STATES>
+// D/16 x D/16 of the state.  The state's values stay in registers and a copy in
+// shared memory feeds the products; the keys are stored twice, plain and
+// weighted, so that a chunk needs three barriers: tiles written, scores
+// written, tiles read.  Everything is an fp32 FMA: bf16 or tf32 parts of fp32
+// operands would need six tensor products to keep this accuracy.  Bound: shared
+// memory reads (60% of their peak) and FMA issue (40%).
+// STATES: local states only (phase 1).
+template <int D, bool STATES>
 __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
     using Cfg = SimtCfg<D>;
-    constexpr int C = Cfg::C, P = Cfg::P, PP = Cfg::PP, W = D / 16, VN = Vec16<T>::N;
+    constexpr int C = Cfg::C, P = Cfg::P, PP = Cfg::PP, W = D / 16;
+    constexpr int FAR = 64, X0 = W <= 4 ? W : 4;  // a thread's columns: X0 tx and, at D = 128, 64 + 4 tx
     extern __shared__ float4 smem4[];
-    float *sq = reinterpret_cast<float *>(smem4), *sk = sq + C * P, *sv = sk + C * P, *sp = sv + C * P,
-          *ss = sp + C * PP, *pw = ss + D * P;  // pw[n] = g^n, n <= C
+    float *sq = reinterpret_cast<float *>(smem4), *sk = sq + C * P, *sv = sk + C * P, *sw = sv + C * P, *sp = sw + C * P,
+          *ss = sp + C * PP, *pw = ss + D * P;  // sw: weighted keys; pw[n] = g^n, n <= C
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int per = STATES ? a.nseg - 1 : a.nseg;
     const int bh = blockIdx.x / per, seg = blockIdx.x - bh * per;
@@ -91,8 +62,7 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
     float *wsp = a.ws + (size_t)bh * a.nseg * D * D;
     float *pool = a.S && slot >= 0 ? a.S + ((size_t)slot * a.H + h) * D * D : nullptr;
     if (tid <= C) pw[tid] = decay_pow(lg, (float)tid);
-    // column of the w-th value of this thread's W columns (16-byte pieces 64 columns apart)
-    auto col = [&](int w) { return W <= 4 ? tx * W + w : 64 * (w >> 2) + 4 * tx + (w & 3); };
+    auto col = [&](int w) { return X0 * tx + (w < 4 ? w : FAR + w - 4); };
     float st[W][W];  // state rows ty * W + r, columns col(w)
 #pragma unroll
     for (int r = 0; r < W; ++r)
@@ -121,31 +91,46 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
             }
         }
     }
-    const T *qp = static_cast<const T *>(a.q) + b * a.lq.batch + h * a.lq.head;
-    const T *kp = static_cast<const T *>(a.k) + b * a.lk.batch + h * a.lk.head;
-    const T *vp = static_cast<const T *>(a.v) + b * a.lv.batch + h * a.lv.head;
-    T *op = static_cast<T *>(a.o) + b * a.lo.batch + h * a.lo.head;
+    const float *qp = static_cast<const float *>(a.q) + b * a.lq.batch + h * a.lq.head;
+    const float *kp = static_cast<const float *>(a.k) + b * a.lk.batch + h * a.lk.head;
+    const float *vp = static_cast<const float *>(a.v) + b * a.lv.batch + h * a.lv.head;
+    float *op = static_cast<float *>(a.o) + b * a.lo.batch + h * a.lo.head;
     const DecaySplit whole(lg, (float)C);
+    // acc += A rows (4 ty ...) x B, over `kend` columns of A
+    auto product = [&](const float *A, int lda, const float *Bm, int kend, float (&acc)[4][W]) {
+        for (int j = 0; j < kend; j += 4) {
+            float av[4][4];
+#pragma unroll
+            for (int ii = 0; ii < 4; ++ii) lds_vec<4>(A + (4 * ty + ii) * lda + j, 0, av[ii]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float bv[W];
+                lds_vec<W>(Bm + (j + u) * P + X0 * tx, FAR, bv);
+#pragma unroll
+                for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+                    for (int w = 0; w < W; ++w) acc[ii][w] = fmaf(av[ii][u], bv[w], acc[ii][w]);
+            }
+        }
+    };
     for (int n0 = begin; n0 < end; n0 += C) {
         const int n = min(C, end - n0);  // tokens of this chunk
         __syncthreads();
-        for (int i = tid; i < C * (D / VN); i += 256) {
-            const int r = i / (D / VN), c = (i - r * (D / VN)) * VN;
-            float f[VN];
-            auto put = [&](float *dst) {
-#pragma unroll
-                for (int u = 0; u < VN; u += 4)
-                    *reinterpret_cast<float4 *>(dst + r * P + c + u) = make_float4(f[u], f[u + 1], f[u + 2], f[u + 3]);
+#pragma unroll 4
+        for (int i = tid; i < C * (D / 4); i += 256) {
+            const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+            auto get = [&](const float *src, long long tok) {
+                return r < n ? *reinterpret_cast<const float4 *>(src + (long long)(n0 + r) * tok + c) : zero;
             };
-            auto get = [&](const T *src, long long tok) {
-                if (r < n) Vec16<T>::load(src + (long long)(n0 + r) * tok + c, f);
-                else
-#pragma unroll
-                    for (int u = 0; u < VN; ++u) f[u] = 0.f;
-            };
-            get(kp, a.lk.tok), put(sk);
-            get(vp, a.lv.tok), put(sv);
-            if (!STATES) get(qp, a.lq.tok), put(sq);
+            const float4 k = get(kp, a.lk.tok), v = get(vp, a.lv.tok);
+            const float f = pw[max(n - 1 - r, 0)];
+            *reinterpret_cast<float4 *>(sv + r * P + c) = v;
+            *reinterpret_cast<float4 *>(sw + r * P + c) = make_float4(f * k.x, f * k.y, f * k.z, f * k.w);
+            if (!STATES) {
+                *reinterpret_cast<float4 *>(sk + r * P + c) = k;
+                *reinterpret_cast<float4 *>(sq + r * P + c) = get(qp, a.lq.tok);
+            }
         }
         if (!STATES) {
 #pragma unroll
@@ -166,12 +151,12 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
             for (int c = 0; c < D; c += 4) {
                 float qv[4][4];
 #pragma unroll
-                for (int ii = 0; ii < 4; ++ii) lds_vec<4>(sq + (4 * ty + ii) * P + c, qv[ii]);
+                for (int ii = 0; ii < 4; ++ii) lds_vec<4>(sq + (4 * ty + ii) * P + c, 0, qv[ii]);
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
                     if (16 * jj < jmax) {
                         float kv[4];
-                        lds_vec<4>(sk + (tx + 16 * jj) * P + c, kv);
+                        lds_vec<4>(sk + (tx + 16 * jj) * P + c, 0, kv);
 #pragma unroll
                         for (int ii = 0; ii < 4; ++ii)
 #pragma unroll
@@ -186,63 +171,29 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
                     const int i = 4 * ty + ii, j = tx + 16 * jj;
                     sp[i * PP + j] = j <= i ? acc[ii][jj] * pw[i - j] : 0.f;
                 }
-            __syncthreads();
-            float out[4][W], in[4][W];
+            float out[4][W];
 #pragma unroll
             for (int ii = 0; ii < 4; ++ii)
 #pragma unroll
-                for (int w = 0; w < W; ++w) out[ii][w] = in[ii][w] = 0.f;
-            auto product = [&](const float *A, int lda, const float *Bm, int kend, float (&acc)[4][W]) {
-                for (int j = 0; j < kend; j += 4) {
-                    float av[4][4];
+                for (int w = 0; w < W; ++w) out[ii][w] = 0.f;
+            product(sq, P, ss, D, out);
 #pragma unroll
-                    for (int ii = 0; ii < 4; ++ii) lds_vec<4>(A + (4 * ty + ii) * lda + j, av[ii]);
+            for (int ii = 0; ii < 4; ++ii)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        float bv[W];
-                        if constexpr (W <= 4) {
-                            lds_vec<W>(Bm + (j + u) * P + tx * W, bv);
-                        } else {
-                            float x[4];
-                            lds_vec<4>(Bm + (j + u) * P + 4 * tx, x);
-                            bv[0] = x[0], bv[1] = x[1], bv[2] = x[2], bv[3] = x[3];
-                            lds_vec<4>(Bm + (j + u) * P + 64 + 4 * tx, x);
-                            bv[4] = x[0], bv[5] = x[1], bv[6] = x[2], bv[7] = x[3];
-                        }
-#pragma unroll
-                        for (int ii = 0; ii < 4; ++ii)
-#pragma unroll
-                            for (int w = 0; w < W; ++w) acc[ii][w] = fmaf(av[ii][u], bv[w], acc[ii][w]);
-                    }
-                }
-            };
+                for (int w = 0; w < W; ++w) out[ii][w] *= pw[4 * ty + ii + 1];
+            __syncthreads();
             product(sp, PP, sv, jmax, out);
-            product(sq, P, ss, D, in);
 #pragma unroll
             for (int ii = 0; ii < 4; ++ii) {
                 const int i = 4 * ty + ii;
                 if (i < n) {
-                    T *dst = op + (long long)(n0 + i) * a.lo.tok;
-                    const float f = pw[i + 1];
+                    float *dst = op + (long long)(n0 + i) * a.lo.tok;
 #pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        const float x = a.scale * fmaf(f, in[ii][w], out[ii][w]);
-                        if constexpr (sizeof(T) == 2) dst[col(w)] = __float2bfloat16_rn(x);
-                        else dst[col(w)] = x;
-                    }
+                    for (int w = 0; w < W; ++w) dst[col(w)] = a.scale * out[ii][w];
                 }
             }
         }
-        // the values, weighted by their distance to the chunk's end
-        __syncthreads();
-        for (int i = tid; i < n * (D / 4); i += 256) {
-            const int j = i / (D / 4);
-            float4 *x = reinterpret_cast<float4 *>(sv + j * P + 4 * (i - j * (D / 4)));
-            const float f = pw[n - 1 - j];
-            *x = make_float4(f * x->x, f * x->y, f * x->z, f * x->w);
-        }
-        __syncthreads();
-        // state: the chunk's decay, then its tokens
+        // state: the chunk's decay and its tokens
         DecaySplit g = whole;
         if (n < C) g = DecaySplit(lg, (float)n);
         float add[W][W];
@@ -253,16 +204,8 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
 #pragma unroll 4
         for (int j = 0; j < n; ++j) {
             float kv[W], vv[W];
-            lds_vec<W>(sk + j * P + ty * W, kv);
-            if constexpr (W <= 4) {
-                lds_vec<W>(sv + j * P + tx * W, vv);
-            } else {
-                float x[4];
-                lds_vec<4>(sv + j * P + 4 * tx, x);
-                vv[0] = x[0], vv[1] = x[1], vv[2] = x[2], vv[3] = x[3];
-                lds_vec<4>(sv + j * P + 64 + 4 * tx, x);
-                vv[4] = x[0], vv[5] = x[1], vv[6] = x[2], vv[7] = x[3];
-            }
+            lds_vec<W>(sw + j * P + ty * W, 4, kv);
+            lds_vec<W>(sv + j * P + X0 * tx, FAR, vv);
 #pragma unroll
             for (int r = 0; r < W; ++r)
 #pragma unroll
@@ -273,26 +216,19 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
 #pragma unroll
             for (int w = 0; w < W; ++w) st[r][w] = fmaf(st[r][w], g.hi, fmaf(st[r][w], g.lo, add[r][w]));
     }
-    if (STATES) {
-        float *dst = wsp + (size_t)(seg + 1) * D * D;
+    if (STATES || (pool && begin < L && end == L)) {
+        float *dst = STATES ? wsp + (size_t)(seg + 1) * D * D : pool;
 #pragma unroll
         for (int r = 0; r < W; ++r)
 #pragma unroll
             for (int w = 0; w < W; ++w) dst[(ty * W + r) * D + col(w)] = st[r][w];
-        return;
     }
-    if (pool && begin < L && end == L) {
-#pragma unroll
-        for (int r = 0; r < W; ++r)
-#pragma unroll
-            for (int w = 0; w < W; ++w) pool[(ty * W + r) * D + col(w)] = st[r][w];
-    }
-    // rows past the prompt's end are zeros
-    const float zero[VN] = {};
-    const int z0 = max(begin, L), z1 = min(begin + a.seg, a.N);
-    for (long long i = tid; i < (long long)(z1 - z0) * (D / VN); i += 256) {
-        const int r = (int)(i / (D / VN)), c = (int)(i - (long long)r * (D / VN)) * VN;
-        Vec16<T>::store(op + (long long)(z0 + r) * a.lo.tok + c, zero);
+    if (!STATES) {  // rows past the prompt's end are zeros
+        const int z0 = max(begin, L), z1 = min(begin + a.seg, a.N);
+        for (long long i = tid; i < (long long)(z1 - z0) * (D / 4); i += 256) {
+            const int r = (int)(i / (D / 4)), c = (int)(i - (long long)r * (D / 4)) * 4;
+            *reinterpret_cast<float4 *>(op + (long long)(z0 + r) * a.lo.tok + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
     }
 }
 
