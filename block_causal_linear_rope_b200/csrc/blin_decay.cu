@@ -38,13 +38,13 @@ static cudaError_t launch_prompt(const DecayArgs &a, int states_threads, int sta
 }
 
 template <int D>
-static cudaError_t simt(const DecayArgs &a, cudaStream_t s) {
-    constexpr int smem = SimtCfg<D>::BYTES;
-    return launch_prompt<decay_simt_kernel<D, true>, decay_simt_kernel<D, false>>(a, 256, smem, 256, smem, s);
+static cudaError_t f32(const DecayArgs &a, cudaStream_t s) {
+    constexpr int smem = F32Cfg<D>::BYTES;
+    return launch_prompt<decay_f32_kernel<D, true>, decay_f32_kernel<D, false>>(a, 256, smem, 256, smem, s);
 }
 
-cudaError_t launch_decay_simt(const DecayArgs &a, int d, cudaStream_t s) {
-    return d == 32 ? simt<32>(a, s) : d == 64 ? simt<64>(a, s) : simt<128>(a, s);
+cudaError_t launch_decay_f32(const DecayArgs &a, int d, cudaStream_t s) {
+    return d == 32 ? f32<32>(a, s) : d == 64 ? f32<64>(a, s) : f32<128>(a, s);
 }
 
 // The warpgroups that take more registers draw on what the kernel was launched with: a build with fewer
@@ -135,7 +135,7 @@ static Split split_prompt(long long heads, int N, int chunk, int resident) {
 static Split split_of(int B, int H, int N, int d, blin_dtype dt) {
     // CTAs that share an SM: by shared memory
     if (dt == BLIN_BF16) return split_prompt((long long)B * H, N, 128, d == 32 ? 2 : 1);
-    return split_prompt((long long)B * H, N, kSimtChunk, d == 128 ? 1 : d == 64 ? 2 : 4);
+    return split_prompt((long long)B * H, N, kF32Chunk, d == 128 ? 1 : d == 64 ? 2 : 4);
 }
 
 static size_t workspace_of(const Split &sp, int B, int H, int d) {
@@ -223,7 +223,7 @@ blin_status blin_decay_prefill(const void *q, const void *k, const void *v, void
     a.ws = static_cast<float *>(workspace);
     if ((a.wd = watchdog_ptr()) == nullptr) return failf(BLIN_ERR_CUDA, "no CUDA device");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return launched(dt == BLIN_BF16 ? launch_decay_tc(a, d, s) : launch_decay_simt(a, d, s), "decayed attention launch");
+    return launched(dt == BLIN_BF16 ? launch_decay_tc(a, d, s) : launch_decay_f32(a, d, s), "decayed attention launch");
 }
 
 blin_status blin_decay_step(const void *q, const void *k, const void *v, void *o, blin_dtype dt, int B, int H, int d,

@@ -102,8 +102,8 @@ __device__ __forceinline__ int decay_len(const DecayArgs &a, int b) {
     return a.lengths ? min(max(__ldg(a.lengths + b), 0), a.N) : a.N;
 }
 
-// Prompts: fp32 on the CUDA cores (kern_decay.cuh), bf16 on the tensor cores (kern_decay_tc.cuh).
-cudaError_t launch_decay_simt(const DecayArgs &a, int d, cudaStream_t s);
+// Prompts: fp32 in tf32 parts (kern_decay.cuh), bf16 on tcgen05 (kern_decay_tc.cuh).
+cudaError_t launch_decay_f32(const DecayArgs &a, int d, cudaStream_t s);
 cudaError_t launch_decay_tc(const DecayArgs &a, int d, cudaStream_t s);
 cudaError_t launch_decay_step(const DecayArgs &a, int d, bool bf16, cudaStream_t s);
 

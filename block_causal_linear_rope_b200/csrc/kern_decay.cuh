@@ -1,5 +1,4 @@
-// Decayed linear attention on the CUDA cores: prompts in fp32 arithmetic, and
-// the single-token step of both types.
+// Decayed linear attention: fp32 prompts, and the single-token step of both types.
 #pragma once
 
 #include "decay.cuh"
@@ -7,51 +6,95 @@
 namespace blin {
 
 // ---------------------------------------------------------------------------- prompts
-constexpr int kSimtChunk = 64;
+constexpr int kF32Chunk = 64;
 
 template <int D>
-struct SimtCfg {
-    static constexpr int C = kSimtChunk, P = D + 4;  // rows padded by 16 bytes: no bank conflicts on 16-byte reads
-    static constexpr int PP = C + 4;
-    static constexpr int FLOATS = 4 * C * P + C * PP + D * P + C + 4;
+struct F32Cfg {
+    static constexpr int C = kF32Chunk;
+    // row pitches in floats: an operand read along its rows wants 4 (mod 32), one read down its columns 8, so
+    // that the 32 lanes of a fragment load hit 32 banks
+    static constexpr int PR = D + 4, PC = D + 8, PP = C + 4;
+    static constexpr int FLOATS = 2 * C * PR + 2 * C * PC + D * PC + C * PP + C + 4;
     static constexpr int BYTES = FLOATS * 4;
+    // warps of a D x D product: rows x columns, and 16 x 8 tiles of a warp
+    static constexpr int SM = D == 32 ? 2 : 4, SN = 8 / SM, MT = D / (16 * SM), NT = D / (8 * SN);
+    static constexpr int OT = D / 16;  // tiles of a warp's outputs (16 rows x D/2 columns)
 };
 
-// V consecutive floats of shared memory, 16 bytes at a time, the second 16 bytes `far` floats on.
-template <int V>
-__device__ __forceinline__ void lds_vec(const float *p, int far, float (&f)[V]) {
-    if constexpr (V == 2) {
-        const float2 v = *reinterpret_cast<const float2 *>(p);
-        f[0] = v.x, f[1] = v.y;
-    } else {
+// x as hi + lo with hi rounded to tf32 (10 fraction bits) and lo the exact rest, of which the tensor core
+// drops what is below 2^-21 of x.
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+    hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// acc += A (16 rows, `kend` columns) x B (`kend` rows, 8 N columns) by one warp, tiles n < live only.
+// AT: A is stored with its columns as rows; BT: B is.  The tensor core rounds its running sums towards zero;
+// the two small products have sums of their own, so that the large one's see one rounding per 8 columns, and
+// three products in a row go to different sums.
+template <int N, bool AT, bool BT>
+__device__ __forceinline__ void f32_product(const float *A, int pa, const float *B, int pb, int kend, float (&acc)[N][4],
+                                            int live) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float small[N][4] = {};
+#pragma unroll 2
+    for (int k = 0; k < kend; k += 8) {
+        uint32_t ah[4], al[4], bh[N][2], bl[N][2];
 #pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-            const float4 v = *reinterpret_cast<const float4 *>(p + far * i);
-            f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
+        for (int i = 0; i < 4; ++i) {
+            const int r = g + 8 * (i & 1), c = k + t + 4 * (i >> 1);
+            split_tf32(AT ? A[c * pa + r] : A[r * pa + c], ah[i], al[i]);
         }
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (n < live)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = k + t + 4 * i, c = 8 * n + g;
+                    split_tf32(BT ? B[c * pb + r] : B[r * pb + c], bh[n][i], bl[n][i]);
+                }
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (n < live) mma_tf32(acc[n], ah, bh[n]);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (n < live) mma_tf32(small[n], al, bh[n]);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (n < live) mma_tf32(small[n], ah, bl[n]);
     }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] += small[n][i];
 }
 
 // One segment of one fp32 head, 64 tokens at a time:
 //   o_i = scale (sum_{j <= i} g^{i-j} (q_i . k_j) v_j + g^{i+1} q_i S),
 //   S  <- g^n S + sum_j (g^{n-1-j} k_j)^T v_j.
-// 16 x 16 threads hold a 4 x 4 tile of the scores, 4 x D/16 of the outputs and
-// D/16 x D/16 of the state.  The state's values stay in registers and a copy in
-// shared memory feeds the products; the keys are stored twice, plain and
-// weighted, so that a chunk needs three barriers: tiles written, scores
-// written, tiles read.  Everything is an fp32 FMA: bf16 or tf32 parts of fp32
-// operands would need six tensor products to keep this accuracy.  Bound: shared
-// memory reads (60% of their peak) and FMA issue (40%).
-// STATES: local states only (phase 1).
+// fp32 has no tensor product of its own, and FMAs alone bound the chunk at 6700
+// cycles of a whole SM (d = 64; 177 us for 2 x 16 heads x 4000 tokens).  Each
+// operand is split in registers into two tf32 parts as it is read from shared
+// memory, and three products (hi hi + hi lo + lo hi) keep 21 bits of it: what is
+// dropped is below 2^-21 a term, unbiased, where the sums' own rounding is 2^-22
+// to 2^-21.  A chunk's state product is summed from zero and added to the
+// decayed state, which stays in fp32 registers, by FMAs: the tensor core rounds
+// its running sums towards zero, and a long-lived state must not collect that.
+// Eight warps share each product; the keys are stored twice, plain and weighted,
+// so that a chunk needs three barriers.  STATES: local states only (phase 1).
 template <int D, bool STATES>
-__global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
-    using Cfg = SimtCfg<D>;
-    constexpr int C = Cfg::C, P = Cfg::P, PP = Cfg::PP, W = D / 16;
-    constexpr int FAR = 64, X0 = W <= 4 ? W : 4;  // a thread's columns: X0 tx and, at D = 128, 64 + 4 tx
+__global__ void __launch_bounds__(256) decay_f32_kernel(const DecayArgs a) {
+    using Cfg = F32Cfg<D>;
+    constexpr int C = Cfg::C, PR = Cfg::PR, PC = Cfg::PC, PP = Cfg::PP, MT = Cfg::MT, NT = Cfg::NT, OT = Cfg::OT;
     extern __shared__ float4 smem4[];
-    float *sq = reinterpret_cast<float *>(smem4), *sk = sq + C * P, *sv = sk + C * P, *sw = sv + C * P, *sp = sw + C * P,
-          *ss = sp + C * PP, *pw = ss + D * P;  // sw: weighted keys; pw[n] = g^n, n <= C
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    float *sq = reinterpret_cast<float *>(smem4), *sk = sq + C * PR, *sv = sk + C * PR, *sw = sv + C * PC, *ss = sw + C * PC,
+          *sp = ss + D * PC, *pw = sp + C * PP;  // sw: weighted keys; ss: the entering state; pw[n] = g^n, n <= C
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t2 = 2 * (lane & 3);
     const int per = STATES ? a.nseg - 1 : a.nseg;
     const int bh = blockIdx.x / per, seg = blockIdx.x - bh * per;
     const int b = bh / a.H, h = bh - b * a.H;
@@ -62,166 +105,106 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayArgs a) {
     float *wsp = a.ws + (size_t)bh * a.nseg * D * D;
     float *pool = a.S && slot >= 0 ? a.S + ((size_t)slot * a.H + h) * D * D : nullptr;
     if (tid <= C) pw[tid] = decay_pow(lg, (float)tid);
-    auto col = [&](int w) { return X0 * tx + (w < 4 ? w : FAR + w - 4); };
-    float st[W][W];  // state rows ty * W + r, columns col(w)
+    // this warp's part of the state: element (m, n, i) is row srow + 16 m + 8 (i >> 1), column scol + 8 n + (i & 1)
+    const int s0 = 16 * MT * (warp / Cfg::SN), s1 = 8 * NT * (warp % Cfg::SN), srow = s0 + g4, scol = s1 + t2;
+    float st[MT][NT][4];
+    auto each = [&](auto &&f) {  // pairs of neighbouring columns
 #pragma unroll
-    for (int r = 0; r < W; ++r)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int w = 0; w < W; ++w) st[r][w] = 0.f;
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) f(srow + 16 * m + 4 * i, scol + 8 * n, st[m][n][i], st[m][n][i + 1]);
+    };
+    each([&](int, int, float &x, float &y) { x = y = 0.f; });
     if (STATES) {
         if (seg == 0)  // the second launch may overwrite the pool while others still read the entering state
             for (int i = tid; i < D * D / 4; i += 256)
                 reinterpret_cast<float4 *>(wsp)[i] =
                     pool ? reinterpret_cast<const float4 *>(pool)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
     } else if (begin < L) {
-        if (a.nseg == 1) {
-            if (pool)
-#pragma unroll
-                for (int r = 0; r < W; ++r)
-#pragma unroll
-                    for (int w = 0; w < W; ++w) st[r][w] = pool[(ty * W + r) * D + col(w)];
-        } else {
-            for (int s = 0; s <= seg; ++s) {
-                const float f = decay_pow(lg, (float)(begin - s * a.seg));
-#pragma unroll
-                for (int r = 0; r < W; ++r)
-#pragma unroll
-                    for (int w = 0; w < W; ++w)
-                        st[r][w] = fmaf(f, wsp[(size_t)s * D * D + (ty * W + r) * D + col(w)], st[r][w]);
-            }
-        }
+        auto add = [&](const float *src, float f) {
+            each([&](int r, int c, float &x, float &y) {
+                const float2 v = *reinterpret_cast<const float2 *>(src + r * D + c);
+                x = fmaf(f, v.x, x), y = fmaf(f, v.y, y);
+            });
+        };
+        if (a.nseg > 1)
+            for (int s = 0; s <= seg; ++s) add(wsp + (size_t)s * D * D, decay_pow(lg, (float)(begin - s * a.seg)));
+        else if (pool) add(pool, 1.f);
     }
     const float *qp = static_cast<const float *>(a.q) + b * a.lq.batch + h * a.lq.head;
     const float *kp = static_cast<const float *>(a.k) + b * a.lk.batch + h * a.lk.head;
     const float *vp = static_cast<const float *>(a.v) + b * a.lv.batch + h * a.lv.head;
     float *op = static_cast<float *>(a.o) + b * a.lo.batch + h * a.lo.head;
     const DecaySplit whole(lg, (float)C);
-    // acc += A rows (4 ty ...) x B, over `kend` columns of A
-    auto product = [&](const float *A, int lda, const float *Bm, int kend, float (&acc)[4][W]) {
-        for (int j = 0; j < kend; j += 4) {
-            float av[4][4];
-#pragma unroll
-            for (int ii = 0; ii < 4; ++ii) lds_vec<4>(A + (4 * ty + ii) * lda + j, 0, av[ii]);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                float bv[W];
-                lds_vec<W>(Bm + (j + u) * P + X0 * tx, FAR, bv);
-#pragma unroll
-                for (int ii = 0; ii < 4; ++ii)
-#pragma unroll
-                    for (int w = 0; w < W; ++w) acc[ii][w] = fmaf(av[ii][u], bv[w], acc[ii][w]);
-            }
-        }
-    };
+    const int wr = warp >> 1, wc = warp & 1, i0 = 16 * wr + g4;  // scores and outputs: 4 x 2 warps, rows i0 and i0 + 8
     for (int n0 = begin; n0 < end; n0 += C) {
         const int n = min(C, end - n0);  // tokens of this chunk
         __syncthreads();
 #pragma unroll 4
         for (int i = tid; i < C * (D / 4); i += 256) {
             const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
-            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
             auto get = [&](const float *src, long long tok) {
-                return r < n ? *reinterpret_cast<const float4 *>(src + (long long)(n0 + r) * tok + c) : zero;
+                return r < n ? *reinterpret_cast<const float4 *>(src + (long long)(n0 + r) * tok + c) : make_float4(0.f, 0.f, 0.f, 0.f);
             };
             const float4 k = get(kp, a.lk.tok), v = get(vp, a.lv.tok);
             const float f = pw[max(n - 1 - r, 0)];
-            *reinterpret_cast<float4 *>(sv + r * P + c) = v;
-            *reinterpret_cast<float4 *>(sw + r * P + c) = make_float4(f * k.x, f * k.y, f * k.z, f * k.w);
+            *reinterpret_cast<float4 *>(sv + r * PC + c) = v;
+            *reinterpret_cast<float4 *>(sw + r * PC + c) = make_float4(f * k.x, f * k.y, f * k.z, f * k.w);
             if (!STATES) {
-                *reinterpret_cast<float4 *>(sk + r * P + c) = k;
-                *reinterpret_cast<float4 *>(sq + r * P + c) = get(qp, a.lq.tok);
+                *reinterpret_cast<float4 *>(sk + r * PR + c) = k;
+                *reinterpret_cast<float4 *>(sq + r * PR + c) = get(qp, a.lq.tok);
             }
         }
-        if (!STATES) {
-#pragma unroll
-            for (int r = 0; r < W; ++r)
-#pragma unroll
-                for (int w = 0; w < W; ++w) ss[(ty * W + r) * P + col(w)] = st[r][w];
-        }
+        if (!STATES)
+            each([&](int r, int c, float &x, float &y) { *reinterpret_cast<float2 *>(ss + r * PC + c) = make_float2(x, y); });
         __syncthreads();
         if (!STATES) {
-            // a warp's rows end at 8 warp + 7: columns past them are masked and skipped
-            const int jmax = 8 * (tid >> 5) + 8;
-            float acc[4][4];
+            // a warp's rows end at 16 wr + 15: columns past them are masked, and whole tiles of them skipped
+            float p[4][4] = {};
+            f32_product<4, false, true>(sq + 16 * wr * PR, PR, sk + 32 * wc * PR, PR, D, p, 2 * wr + 2 - 4 * wc);
 #pragma unroll
-            for (int ii = 0; ii < 4; ++ii)
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int jj = 0; jj < 4; ++jj) acc[ii][jj] = 0.f;
-#pragma unroll 2
-            for (int c = 0; c < D; c += 4) {
-                float qv[4][4];
-#pragma unroll
-                for (int ii = 0; ii < 4; ++ii) lds_vec<4>(sq + (4 * ty + ii) * P + c, 0, qv[ii]);
-#pragma unroll
-                for (int jj = 0; jj < 4; ++jj) {
-                    if (16 * jj < jmax) {
-                        float kv[4];
-                        lds_vec<4>(sk + (tx + 16 * jj) * P + c, 0, kv);
-#pragma unroll
-                        for (int ii = 0; ii < 4; ++ii)
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) acc[ii][jj] = fmaf(qv[ii][u], kv[u], acc[ii][jj]);
-                    }
+                for (int i = 0; i < 4; i += 2) {
+                    const int r = i0 + 4 * i, c = 32 * wc + 8 * u + t2;
+                    *reinterpret_cast<float2 *>(sp + r * PP + c) =
+                        make_float2(c <= r ? p[u][i] * pw[r - c] : 0.f, c + 1 <= r ? p[u][i + 1] * pw[r - c - 1] : 0.f);
                 }
-            }
+            float out[OT][4] = {};
+            f32_product<OT, false, false>(sq + 16 * wr * PR, PR, ss + D / 2 * wc, PC, D, out, OT);
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj)
+            for (int u = 0; u < OT; ++u)
 #pragma unroll
-                for (int ii = 0; ii < 4; ++ii) {
-                    const int i = 4 * ty + ii, j = tx + 16 * jj;
-                    sp[i * PP + j] = j <= i ? acc[ii][jj] * pw[i - j] : 0.f;
-                }
-            float out[4][W];
-#pragma unroll
-            for (int ii = 0; ii < 4; ++ii)
-#pragma unroll
-                for (int w = 0; w < W; ++w) out[ii][w] = 0.f;
-            product(sq, P, ss, D, out);
-#pragma unroll
-            for (int ii = 0; ii < 4; ++ii)
-#pragma unroll
-                for (int w = 0; w < W; ++w) out[ii][w] *= pw[4 * ty + ii + 1];
+                for (int i = 0; i < 4; ++i) out[u][i] *= pw[i0 + 8 * (i >> 1) + 1];
             __syncthreads();
-            product(sp, PP, sv, jmax, out);
+            f32_product<OT, false, false>(sp + 16 * wr * PP, PP, sv + D / 2 * wc, PC, 16 * wr + 16, out, OT);
 #pragma unroll
-            for (int ii = 0; ii < 4; ++ii) {
-                const int i = 4 * ty + ii;
-                if (i < n) {
-                    float *dst = op + (long long)(n0 + i) * a.lo.tok;
+            for (int i = 0; i < 4; i += 2)
+                if (i0 + 4 * i < n) {
+                    float *dst = op + (long long)(n0 + i0 + 4 * i) * a.lo.tok + D / 2 * wc + t2;
 #pragma unroll
-                    for (int w = 0; w < W; ++w) dst[col(w)] = a.scale * out[ii][w];
+                    for (int u = 0; u < OT; ++u)
+                        *reinterpret_cast<float2 *>(dst + 8 * u) = make_float2(a.scale * out[u][i], a.scale * out[u][i + 1]);
                 }
-            }
         }
         // state: the chunk's decay and its tokens
         DecaySplit g = whole;
         if (n < C) g = DecaySplit(lg, (float)n);
-        float add[W][W];
 #pragma unroll
-        for (int r = 0; r < W; ++r)
+        for (int m = 0; m < MT; ++m) {
+            float add[NT][4] = {};
+            f32_product<NT, true, false>(sw + s0 + 16 * m, PC, sv + s1, PC, (n + 7) & ~7, add, NT);
 #pragma unroll
-            for (int w = 0; w < W; ++w) add[r][w] = 0.f;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) {
-            float kv[W], vv[W];
-            lds_vec<W>(sw + j * P + ty * W, 4, kv);
-            lds_vec<W>(sv + j * P + X0 * tx, FAR, vv);
+            for (int u = 0; u < NT; ++u)
 #pragma unroll
-            for (int r = 0; r < W; ++r)
-#pragma unroll
-                for (int w = 0; w < W; ++w) add[r][w] = fmaf(kv[r], vv[w], add[r][w]);
+                for (int i = 0; i < 4; ++i) st[m][u][i] = fmaf(st[m][u][i], g.hi, fmaf(st[m][u][i], g.lo, add[u][i]));
         }
-#pragma unroll
-        for (int r = 0; r < W; ++r)
-#pragma unroll
-            for (int w = 0; w < W; ++w) st[r][w] = fmaf(st[r][w], g.hi, fmaf(st[r][w], g.lo, add[r][w]));
     }
     if (STATES || (pool && begin < L && end == L)) {
         float *dst = STATES ? wsp + (size_t)(seg + 1) * D * D : pool;
-#pragma unroll
-        for (int r = 0; r < W; ++r)
-#pragma unroll
-            for (int w = 0; w < W; ++w) dst[(ty * W + r) * D + col(w)] = st[r][w];
+        each([&](int r, int c, float &x, float &y) { *reinterpret_cast<float2 *>(dst + r * D + c) = make_float2(x, y); });
     }
     if (!STATES) {  // rows past the prompt's end are zeros
         const int z0 = max(begin, L), z1 = min(begin + a.seg, a.N);
