@@ -107,14 +107,22 @@ using namespace blin;
 static bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // Segments of a prompt.  A launch runs its units in waves over the SMs, so its
-// time goes as waves x chunks of a segment; the first launch of a split prompt
-// (states only) costs about half as much per chunk as the second.  The split
-// with the smallest sum is taken, from sizes alone.
+// time goes as waves x (chunks of a segment + what a unit costs besides); a split
+// prompt has a first launch (states only) with cheaper chunks, and its second
+// one's units add up the states before them.  The split with the smallest sum is
+// taken, from sizes alone.  The costs are in chunks of the path's second launch
+// as measured on a B200: a chunk of 64 fp32 tokens takes about 7 us, one of 128
+// bf16 tokens 2 to 4 us, and a launch and a unit's start a few us either way (4
+// heads of 300 fp32 tokens: 39 us in one piece, 19 in five; 16 heads of 1024 bf16
+// tokens, d = 64: 23 us in one, 21 in four).
 static constexpr int kSms = 148, kMaxSegments = 32;
 struct Split {
     int nseg, seg;
 };
-static Split split_prompt(long long heads, int N, int chunk, int resident) {
+struct SplitCosts {
+    double unit, join, chunk1, launch1;  // a unit's start, a state it adds, a chunk and the rest of the first launch
+};
+static Split split_prompt(long long heads, int N, int chunk, int resident, const SplitCosts &k) {
     const int nc = std::max(1, (N + chunk - 1) / chunk);
     const long long slots = (long long)kSms * resident;
     Split best{1, nc * chunk};
@@ -123,7 +131,7 @@ static Split split_prompt(long long heads, int N, int chunk, int resident) {
         const int len = (nc + s - 1) / s, n = (nc + len - 1) / len;
         if (n != s || heads * n >= (1LL << 31)) continue;
         const double waves = (double)((heads * n + slots - 1) / slots), first = (double)((heads * (n - 1) + slots - 1) / slots);
-        const double t = waves * (len + 2 + 0.25 * (n - 1)) + first * (0.5 * len + 3);
+        const double t = waves * (len + k.unit + k.join * (n - 1)) + first * (k.chunk1 * len + k.launch1);
         if (s == 1 || t < cost) {
             cost = t;
             best = Split{n, len * chunk};
@@ -133,9 +141,10 @@ static Split split_prompt(long long heads, int N, int chunk, int resident) {
 }
 
 static Split split_of(int B, int H, int N, int d, blin_dtype dt) {
-    // CTAs that share an SM: by shared memory
-    if (dt == BLIN_BF16) return split_prompt((long long)B * H, N, 128, d == 32 ? 2 : 1);
-    return split_prompt((long long)B * H, N, kF32Chunk, d == 128 ? 1 : d == 64 ? 2 : 4);
+    const long long heads = (long long)B * H;
+    if (dt == BLIN_BF16) return split_prompt(heads, N, 128, d == 32 ? 2 : 1, {2.0, 0.25, 0.5, 3.0});
+    return split_prompt(heads, N, kF32Chunk, d == 128 ? F32Cfg<128>::CTAS : d == 64 ? F32Cfg<64>::CTAS : F32Cfg<32>::CTAS,
+                        {0.3, 0.05, 0.4, 0.6});
 }
 
 static size_t workspace_of(const Split &sp, int B, int H, int d) {

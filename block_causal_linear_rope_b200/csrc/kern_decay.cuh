@@ -16,6 +16,7 @@ struct F32Cfg {
     static constexpr int PR = D + 4, PC = D + 8, PP = C + 4;
     static constexpr int FLOATS = 2 * C * PR + 2 * C * PC + D * PC + C * PP + C + 4;
     static constexpr int BYTES = FLOATS * 4;
+    static constexpr int CTAS = D == 128 ? 1 : D == 64 ? 2 : 3;  // per SM
     // warps of a D x D product: rows x columns, and 16 x 8 tiles of a warp
     static constexpr int SM = D == 32 ? 2 : 4, SN = 8 / SM, MT = D / (16 * SM), NT = D / (8 * SN);
     static constexpr int OT = D / 16;  // tiles of a warp's outputs (16 rows x D/2 columns)
@@ -88,7 +89,7 @@ __device__ __forceinline__ void f32_product(const float *A, int pa, const float 
 // Eight warps share each product; the keys are stored twice, plain and weighted,
 // so that a chunk needs three barriers.  STATES: local states only (phase 1).
 template <int D, bool STATES>
-__global__ void __launch_bounds__(256) decay_f32_kernel(const DecayArgs a) {
+__global__ void __launch_bounds__(256, F32Cfg<D>::CTAS) decay_f32_kernel(const DecayArgs a) {
     using Cfg = F32Cfg<D>;
     constexpr int C = Cfg::C, PR = Cfg::PR, PC = Cfg::PC, PP = Cfg::PP, MT = Cfg::MT, NT = Cfg::NT, OT = Cfg::OT;
     extern __shared__ float4 smem4[];
@@ -159,6 +160,15 @@ __global__ void __launch_bounds__(256) decay_f32_kernel(const DecayArgs a) {
         }
         if (!STATES)
             each([&](int r, int c, float &x, float &y) { *reinterpret_cast<float2 *>(ss + r * PC + c) = make_float2(x, y); });
+        // the next chunk's rows on their way into L2 while this one is multiplied
+        for (int i = tid; i < C * (D / 32); i += 256) {
+            const int r = n0 + C + i / (D / 32), c = i % (D / 32) * 32;
+            if (r < end) {
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(kp + (long long)r * a.lk.tok + c));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(vp + (long long)r * a.lv.tok + c));
+                if (!STATES) asm volatile("prefetch.global.L2 [%0];" ::"l"(qp + (long long)r * a.lq.tok + c));
+            }
+        }
         __syncthreads();
         if (!STATES) {
             // a warp's rows end at 16 wr + 15: columns past them are masked, and whole tiles of them skipped
