@@ -7,11 +7,17 @@
 //   state    S   <- g^n S + sum_j k_j^T (g^{n-1-j} v_j)            (d x d, K = 128)
 // All four products run on tcgen05.mma with fp32 accumulators in TMEM.
 //
-// Precision.  P and the S that multiplies q are rounded to bf16 (each product's
-// other operand is bf16 already, and so is the result).  The state itself is
-// fp32 and stays in registers from chunk to chunk; the weighted values
-// g^{n-1-j} v_j of its update are split into three bf16 parts (8 + 8 + 8 bits),
-// so that its product carries fp32 accuracy.
+// Precision.  P is rounded to bf16 (its product's other operand is bf16 already,
+// and so is the result).  The S that multiplies q is handed over in two bf16
+// parts, 16 bits of it: rounded once like P it would double the error that the
+// result's own rounding leaves (2.35e-3 of the outputs' norm against 1.66e-3;
+// with two parts 1.74e-3 for slow decays, 2.1e-3 for fast ones, where P's share
+// is large), and the second part's products cost 6 to 11% of the time at d >= 64
+// and nothing at d = 32.  The state itself is fp32 and stays in registers from
+// chunk to chunk; the weighted values g^{n-1-j} v_j of its update are split into
+// three bf16 parts (8 + 8 + 8 bits), so that its product carries fp32 accuracy
+// (at most 4e-7 of the state's norm, most of it the tensor core's rounding of
+// running sums towards zero).
 //
 // Roles: a TMA producer thread, two MMA issuing threads (scores and outputs,
 // state), warpgroups that weight the scores (TMEM -> registers -> P as bf16 over
@@ -42,14 +48,14 @@ struct DecayTc {
     static constexpr int SUB = C * ROWB, TILE = NAT * SUB;
     static constexpr uint32_t LAYOUT = D == 32 ? 4u : 2u;  // 64B / 128B swizzle
     static constexpr int TPC = STATES ? 2 : 3;             // tiles landed per chunk: V, K (, Q)
-    static constexpr int NSLOT = D != 128 ? 9 : STATES ? 4 : 5;
+    static constexpr int NSLOT = D == 128 ? 4 : 9;
     // weighted values: items of IT tokens, three parts each, in a ring of NVB
     static constexpr int IT = D == 128 ? 16 : D == 64 && STATES ? 32 : 64, NIT = C / IT;
     static constexpr int NVB = !STATES ? 2 : D == 128 ? 8 : D == 64 ? 4 : 2;
     static constexpr int VSUB = IT * ROWB, VPART = NAT * VSUB, VITEM = 3 * VPART;
-    static constexpr int SIMG = 2 * D * D, NSB = D == 128 ? 1 : 2;  // bf16 state images
+    static constexpr int SIMG = 2 * D * D;  // a bf16 state image; there are two, high and low part
     static constexpr int OSTG = STATES || D == 128 ? 0 : TILE;      // output staging (d = 128: in the chunk's Q slot)
-    static constexpr int OFF_V = NSLOT * TILE, OFF_S = OFF_V + NVB * VITEM, OFF_O = OFF_S + (STATES ? 0 : NSB * SIMG);
+    static constexpr int OFF_V = NSLOT * TILE, OFF_S = OFF_V + NVB * VITEM, OFF_O = OFF_S + (STATES ? 0 : 2 * SIMG);
     static constexpr int OFF_CTRL = OFF_O + OSTG;
     static constexpr int NBAR = 2 * NSLOT + 2 * NVB + 13;
     static constexpr int OFF_PW = OFF_CTRL + 512;  // g^n for n = 0 .. 128, then scale g^{31 - m} for m < 32
@@ -122,7 +128,7 @@ struct DecayUnit {
     __device__ uint32_t one(int i) const { return bar(2 * Cf::NSLOT + 2 * Cf::NVB + i); }
     __device__ uint8_t *slot(int t) const { return base + (t % Cf::NSLOT) * Cf::TILE; }
     __device__ uint8_t *vbuf(int i) const { return base + Cf::OFF_V + (i % Cf::NVB) * Cf::VITEM; }
-    __device__ uint8_t *sbuf(int c) const { return base + Cf::OFF_S + (c % Cf::NSB) * Cf::SIMG; }
+    __device__ uint8_t *simg() const { return base + Cf::OFF_S; }
     // tile numbers of chunk c in landing order
     __device__ static int tv(int c) { return Cf::TPC * c; }
     __device__ static int tk(int c) { return Cf::TPC * c + 1; }
@@ -225,10 +231,14 @@ struct DecayUnit {
             ptx::mma_commit(one(B_SFULL));
             if (!wait(sready(c), c >> 1, WD_DC_STATE) || (c > 0 && !wait(one(B_OEMPTY), c - 1, WD_DC_OUT))) break;
             ptx::tc_fence_after_sync();
-            const Operand sd = mnmajor(ptx::smem_u32(sbuf(c)), D * Cf::ROWB);
-            mma<IDO, false>(tmem + Cf::T_OI, qd, sd);
+            const Operand sd = mnmajor(ptx::smem_u32(simg()), D * Cf::ROWB);
+            mma<IDO, false>(tmem + Cf::T_OI, qd, sd + Cf::SIMG);
+            mma<IDO, true>(tmem + Cf::T_OI, qd, sd);
 #pragma unroll
-            for (int kk = 1; kk < D / 16; ++kk) mma<IDO, true>(tmem + Cf::T_OI, qd + kstep(kk), sd + rstep(kk));
+            for (int kk = 1; kk < D / 16; ++kk) {
+                mma<IDO, true>(tmem + Cf::T_OI, qd + kstep(kk), sd + (Cf::SIMG + rstep(kk)));
+                mma<IDO, true>(tmem + Cf::T_OI, qd + kstep(kk), sd + rstep(kk));
+            }
             if (!wait(full(tv(c) % Cf::NSLOT), tv(c) / Cf::NSLOT, WD_DC_FULL) || !wait(one(B_PREADY), c, WD_DC_SCORE)) break;
             ptx::tc_fence_after_sync();
             const Operand vd = mnmajor(ptx::smem_u32(slot(tv(c))), Cf::SUB);
@@ -485,21 +495,34 @@ struct DecayUnit {
             *reinterpret_cast<Run *>(dst + pc.offset(i, lane)) = x;
         }
     }
-    // this thread's part of the state as a bf16 operand image
+    // this thread's part of the state as two bf16 operand images, the rounded state and the rounded rest
     __device__ static void put_state(const float (&st)[Cf::NCOL], uint8_t *img, const Piece &pc, int lane) {
+        auto low = [](float x, float y, uint32_t hi) {
+            return pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+        };
         if constexpr (D == 128) {
 #pragma unroll
             for (int j = 0; j < Cf::NCOL / 8; ++j) {
                 const int q = pc.col0 / 8 + j;
-                const float *s = st + 8 * j;
-                *reinterpret_cast<uint4 *>(img + (q / ROWP) * D * Cf::ROWB + swz_chunk<Cf::AW>(pc.f, q % ROWP)) =
-                    make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+                uint8_t *to = img + (q / ROWP) * D * Cf::ROWB + swz_chunk<Cf::AW>(pc.f, q % ROWP);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = st[8 * j + 2 * i], y = st[8 * j + 2 * i + 1];
+                    hi[i] = pack_bf16x2(x, y);
+                    lo[i] = low(x, y, hi[i]);
+                }
+                *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(to + Cf::SIMG) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
         } else {
 #pragma unroll
-            for (int p = 0; p < Cf::NCOL / 2; ++p)
-                *reinterpret_cast<uint32_t *>(img + swz_chunk<Cf::AW>(pc.f + 8 * (p & 1), pc.col0 / 8 + (p >> 1)) + 4 * (lane & 3)) =
-                    pack_bf16x2(st[2 * p], st[2 * p + 1]);
+            for (int p = 0; p < Cf::NCOL / 2; ++p) {
+                uint8_t *to = img + swz_chunk<Cf::AW>(pc.f + 8 * (p & 1), pc.col0 / 8 + (p >> 1)) + 4 * (lane & 3);
+                const uint32_t hi = pack_bf16x2(st[2 * p], st[2 * p + 1]);
+                *reinterpret_cast<uint32_t *>(to) = hi;
+                *reinterpret_cast<uint32_t *>(to + Cf::SIMG) = low(st[2 * p], st[2 * p + 1], hi);
+            }
         }
         ptx::fence_proxy_async_smem();
     }
@@ -538,7 +561,7 @@ struct DecayUnit {
             for (int i = 0; i < Cf::NCOL; ++i) st[i] = 0.f;
         } else {
             load_state(st, pc, lane);
-            put_state(st, sbuf(0), pc, lane);
+            put_state(st, simg(), pc, lane);
             warp_arrive(sready(0), lane);
         }
         const DecaySplit whole(lg, (float)Cf::C);
@@ -556,11 +579,9 @@ struct DecayUnit {
             warp_arrive(kvempty(c), lane);
             if constexpr (!STATES) {
                 if (c + 1 < nc) {
-                    // the next chunk's image goes where that of chunk c + 1 - NSB was, once that has been
-                    // multiplied (without output warps this warp has waited for it before)
-                    const int u = c + 1 - Cf::NSB;
-                    if (Cf::ZW && u >= 0 && !(ok = wait(ofull(u), u >> 1, WD_DC_OUT))) break;
-                    put_state(st, sbuf(c + 1), pc, lane);
+                    // the next chunk's images go where this one's are, once those have been multiplied
+                    if (!(ok = wait(ofull(c), c >> 1, WD_DC_OUT))) break;
+                    put_state(st, simg(), pc, lane);
                     warp_arrive(sready(c + 1), lane);
                 }
                 if (!Cf::ZW) ok = output_chunk(m, c, uw, lane);
