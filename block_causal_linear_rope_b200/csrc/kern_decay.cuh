@@ -79,7 +79,8 @@ __device__ __forceinline__ void f32_product(const float *A, int pa, const float 
 //   o_i = scale (sum_{j <= i} g^{i-j} (q_i . k_j) v_j + g^{i+1} q_i S),
 //   S  <- g^n S + sum_j (g^{n-1-j} k_j)^T v_j.
 // fp32 has no tensor product of its own, and FMAs alone bound the chunk at 6700
-// cycles of a whole SM (d = 64; 177 us for 2 x 16 heads x 4000 tokens).  Each
+// cycles of a whole SM (d = 64; an FMA form took 177 us for 2 x 16 heads of 4000
+// tokens, this one 132, with the tensor cores and the issue slots half busy).  Each
 // operand is split in registers into two tf32 parts as it is read from shared
 // memory, and three products (hi hi + hi lo + lo hi) keep 21 bits of it: what is
 // dropped is below 2^-21 a term, unbiased, where the sums' own rounding is 2^-22

@@ -9,8 +9,8 @@
 //
 // Precision.  P is rounded to bf16 (its product's other operand is bf16 already,
 // and so is the result).  The S that multiplies q is handed over in two bf16
-// parts, 16 bits of it: rounded once like P it would double the error that the
-// result's own rounding leaves (2.35e-3 of the outputs' norm against 1.66e-3;
+// parts, 16 bits of it: rounded once like P, the two would add as much as the
+// result's own rounding does (2.35e-3 of the outputs' norm against 1.66e-3;
 // with two parts 1.74e-3 for slow decays, 2.1e-3 for fast ones, where P's share
 // is large), and the second part's products cost 6 to 11% of the time at d >= 64
 // and nothing at d = 32.  The state itself is fp32 and stays in registers from
@@ -25,11 +25,23 @@
 // memory), and that own the state and the outputs.  They hand over through
 // mbarriers; every wait is bounded.
 //
-// Power.  The call is bound by memory in bytes, but the tensor cores' work alone
-// can take the card to its power limit and its clock down, so no product is
-// wider than it has to be: a state product has M = 64 rows at d <= 64 (d = 32
-// repeats its 32 features by a leading byte offset of 0, and the threads of each
-// copy take half of the columns).
+// Why 128 tokens: the scores fill the 128 lanes of one product.  A token then
+// costs (256 + 5 d) d multiply-adds, 0.04 ns of the tensor cores at d = 64 and
+// 0.14 at d = 128, where its 8 d bytes cost the memory 0.08 and 0.16.  Why one
+// head per CTA: the state then never leaves the registers, and K, V, Q and O
+// cross the memory once.
+//
+// Measured on a B200, sustained: 4 x 32 heads of 32760 tokens, d = 64: 598 us
+// (3.6 TB/s); 32 heads of 32768, d = 128: 506 us; 70 heads of 32760, d = 32:
+// 242 us.  What bounds it: a chunk takes 3300 cycles of an SM at d = 64 (6500 at
+// d = 128, 3600 for two CTAs at d = 32), the round of score product, weights and
+// value product that one score buffer allows (two made each chunk's tiles stay
+// longer in the landing ring and were slower, 528 against 511 us), at 41% tensor
+// and 47% issue utilisation; and the card's power: it runs at its 1000 W limit at
+// 1.55 to 1.75 GHz (a plain copy of random data alone takes 997 W at 6.4 TB/s),
+// so that less work per chunk shows as a higher clock, not as fewer cycles.  M =
+// 64 state products at d <= 64 (d = 32 repeats its 32 features by a leading byte
+// offset of 0, and the threads of each copy take half of the columns) serve that.
 #pragma once
 
 #include <type_traits>
@@ -516,12 +528,21 @@ struct DecayUnit {
                 *reinterpret_cast<uint4 *>(to + Cf::SIMG) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
         } else {
+            // pairs 4q .. 4q + 3 are four 8 x 8 blocks: rows f and f + 8 of two neighbouring 16-byte pieces
+            const int blk = lane >> 3;
+            const int row = pc.f - (lane >> 2) + 8 * (blk & 1) + (lane & 7);
 #pragma unroll
-            for (int p = 0; p < Cf::NCOL / 2; ++p) {
-                uint8_t *to = img + swz_chunk<Cf::AW>(pc.f + 8 * (p & 1), pc.col0 / 8 + (p >> 1)) + 4 * (lane & 3);
-                const uint32_t hi = pack_bf16x2(st[2 * p], st[2 * p + 1]);
-                *reinterpret_cast<uint32_t *>(to) = hi;
-                *reinterpret_cast<uint32_t *>(to + Cf::SIMG) = low(st[2 * p], st[2 * p + 1], hi);
+            for (int q = 0; q < Cf::NCOL / 8; ++q) {
+                const uint32_t to = ptx::smem_u32(img + swz_chunk<Cf::AW>(row, pc.col0 / 8 + 2 * q + (blk >> 1)));
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = st[8 * q + 2 * i], y = st[8 * q + 2 * i + 1];
+                    hi[i] = pack_bf16x2(x, y);
+                    lo[i] = low(x, y, hi[i]);
+                }
+                ptx::stmatrix_x4(to, hi);
+                ptx::stmatrix_x4(to + Cf::SIMG, lo);
             }
         }
         ptx::fence_proxy_async_smem();

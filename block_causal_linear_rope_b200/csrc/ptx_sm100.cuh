@@ -82,6 +82,15 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     return true;
 }
 
+// ------------------------------------------------------------------ shared-memory matrices
+// Four 8 x 8 blocks of 16-bit elements: lane t holds elements (t / 4, 2 (t % 4) + {0, 1}) of block i in r[i];
+// lane 8 i + j gives the address of row j of block i (16 bytes).  Whole warp.
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
 // ------------------------------------------------------------------ barriers / fences
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
