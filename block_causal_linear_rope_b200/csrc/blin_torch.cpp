@@ -13,6 +13,7 @@
 #include <ATen/ATen.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -96,25 +97,41 @@ const Tensor &given_out(PyObject *o, const Tensor &like) {
     check_out(t, like);
     return t;
 }
-Tensor make(at::IntArrayRef shape, const Tensor &like) { return at::empty(shape, like.options().memory_format(at::MemoryFormat::Contiguous)); }
-
 // [B, H, N, d], or [B, H, d], which has no token stride
 blin_layout layout(const Tensor &t) {
     const auto s = t.strides();
     return blin_layout{t.dim() == 4 ? s[2] : t.size(-1), s[1], s[0]};
 }
 
-// The call's stream: the current one, or the handle that the wrapper hands over.  Memory made here on the
-// current stream is kept until a different one has used it.
-cudaStream_t stream_of(PyObject *o, const Tensor &like, std::initializer_list<const Tensor *> made) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(like.device().index()).stream();
-    cudaStream_t s = static_cast<cudaStream_t>(PyLong_AsVoidPtr(o));
-    if (PyErr_Occurred()) type_error("stream must be a torch.cuda.Stream");
-    const c10::cuda::CUDAStream ext = c10::cuda::getStreamFromExternal(s, like.device().index());
-    for (const Tensor *t : made)
-        if (t->defined()) t->record_stream(ext);
-    return s;
-}
+// The call's stream: the current one, or the handle that the wrapper hands over.  Memory that the call makes
+// belongs to its stream (the current stream's may still be in use there by work that the call's does not wait
+// for); what it returns is kept until the current stream, where it is most likely read, has also done with it.
+class CallStream {
+    c10::cuda::CUDAStream current_, used_;
+    c10::cuda::OptionalCUDAStreamGuard guard_;
+
+    static c10::cuda::CUDAStream chosen(PyObject *o, const c10::cuda::CUDAStream &current) {
+        if (o == Py_None) return current;
+        cudaStream_t s = static_cast<cudaStream_t>(PyLong_AsVoidPtr(o));
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            type_error("stream must be a torch.cuda.Stream");
+        }
+        return s == current.stream() ? current : c10::cuda::getStreamFromExternal(s, current.device_index());
+    }
+
+public:
+    CallStream(PyObject *o, const Tensor &like)
+        : current_(c10::cuda::getCurrentCUDAStream(like.device().index())), used_(chosen(o, current_)) {
+        if (used_ != current_) guard_.reset_stream(used_);
+    }
+    cudaStream_t stream() const { return used_.stream(); }
+    Tensor output(at::IntArrayRef shape, const Tensor &like) const {
+        Tensor t = at::empty(shape, like.options().memory_format(at::MemoryFormat::Contiguous));
+        if (used_ != current_) t.record_stream(current_);
+        return t;
+    }
+};
 int64_t integer(PyObject *o, const char *name) {
     const int64_t v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) {
@@ -194,8 +211,8 @@ struct Call {
         }
         slot_of = static_cast<const int *>(optional(sl, "slots", at::kInt, {B}, q));
     }
-    Tensor output(PyObject *o) const {
-        if (o == Py_None) return make(q.sizes(), q);
+    Tensor output(PyObject *o, const CallStream &on) const {
+        if (o == Py_None) return on.output(q.sizes(), q);
         const Tensor &t = given_out(o, q);
         no_overlap(t, q), no_overlap(t, k), no_overlap(t, v);
         if (state) no_overlap(t, *state);
@@ -214,7 +231,8 @@ PyObject *decay_prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Call c(a, 4, "[B, H, N, d]", a[4], a[5]);
         const int64_t N = c.q.size(2);
         const int *lengths = static_cast<const int *>(optional(a[6], "lengths", at::kInt, {c.B}, c.q));
-        const Tensor out = c.output(a[8]);
+        const CallStream on(a[10], c.q);
+        const Tensor out = c.output(a[8], on);
         if (N == 0 && c.B > 0 && c.H > 0) return THPVariable_Wrap(out);  // no tokens: nothing to read, no address to give
         const size_t need = blin_decay_workspace_size((int)c.B, (int)c.H, (int)N, (int)c.d, c.dt);
         Tensor scratch;
@@ -232,12 +250,11 @@ PyObject *decay_prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
             ws = scratch.data_ptr();
             ws_bytes = need;
         }
-        const Tensor made = a[8] == Py_None ? out : Tensor();
-        const cudaStream_t s = stream_of(a[10], c.q, {&made, &scratch});
         const blin_decay_layouts lay = c.layouts(out);
         return answer(blin_decay_prefill(c.q.const_data_ptr(), c.k.const_data_ptr(), c.v.const_data_ptr(), out.data_ptr(), c.dt,
                                          (int)c.B, (int)c.H, (int)N, (int)c.d, c.lg, number(a[7], "scale"),
-                                         c.dense(out) ? nullptr : &lay, lengths, c.pool, (int)c.slots, c.slot_of, ws, ws_bytes, s),
+                                         c.dense(out) ? nullptr : &lay, lengths, c.pool, (int)c.slots, c.slot_of, ws, ws_bytes,
+                                         on.stream()),
                       out);
     });
 }
@@ -248,13 +265,12 @@ PyObject *decay_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
         expect_args(n, 9);
         const Call c(a, 3, "[B, H, d]", a[4], a[5]);
         if (c.state == nullptr) value_error("a step needs a state");
-        const Tensor out = c.output(a[7]);
-        const Tensor made = a[7] == Py_None ? out : Tensor();
-        const cudaStream_t s = stream_of(a[8], c.q, {&made});
+        const CallStream on(a[8], c.q);
+        const Tensor out = c.output(a[7], on);
         const blin_decay_layouts lay = c.layouts(out);
         return answer(blin_decay_step(c.q.const_data_ptr(), c.k.const_data_ptr(), c.v.const_data_ptr(), out.data_ptr(), c.dt,
                                       (int)c.B, (int)c.H, (int)c.d, c.lg, number(a[6], "scale"), c.dense(out) ? nullptr : &lay,
-                                      c.pool, (int)c.slots, c.slot_of, s),
+                                      c.pool, (int)c.slots, c.slot_of, on.stream()),
                       out);
     });
 }
@@ -288,11 +304,16 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
             g.T = t[0], g.Hgt = t[1], g.Wid = t[2];
         }
         const int inverse = PyObject_IsTrue(a[7]);
-        Tensor out[2], made[2];
+        if (inverse < 0) {
+            PyErr_Clear();
+            type_error("inverse must be True or False");
+        }
+        const CallStream on(a[9], q);
+        Tensor out[2];
         const Tensor *in[2] = {&q, &k};
         const int outs = two ? 2 : 1;
         if (a[8] == Py_None) {
-            for (int i = 0; i < outs; ++i) made[i] = out[i] = make(in[i]->sizes(), q);
+            for (int i = 0; i < outs; ++i) out[i] = on.output(in[i]->sizes(), q);
         } else {
             PyObject *o[2] = {a[8], nullptr};
             const bool seq = PyTuple_Check(a[8]) || PyList_Check(a[8]);
@@ -315,13 +336,12 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
             return both;
         };
         if (N == 0 && B > 0 && q.size(1) > 0 && k.size(1) > 0) return result();
-        const cudaStream_t s = stream_of(a[9], q, {&made[0], &made[1]});
         const bool dense = q.is_contiguous() && k.is_contiguous() && out[0].is_contiguous() && out[1].is_contiguous();
         const blin_rope_layouts lay{layout(q), layout(out[0]), layout(k), layout(out[1])};
         const blin_status rc =
             blin_rope(q.const_data_ptr(), out[0].data_ptr(), (int)q.size(1), two ? k.const_data_ptr() : nullptr,
                       two ? out[1].data_ptr() : nullptr, two ? (int)k.size(1) : 0, dt, (int)B, (int)N, (int)d, &g,
-                      (int)integer(a[4], "t0"), pos, shared, inverse, dense ? nullptr : &lay, s);
+                      (int)integer(a[4], "t0"), pos, shared, inverse, dense ? nullptr : &lay, on.stream());
         return rc == BLIN_OK ? result() : PyLong_FromLong(rc);
     });
 }

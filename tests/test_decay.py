@@ -327,3 +327,54 @@ def test_rope_prompt_and_steps_together(blin):
     assert (abs(f64(torch.cat(outs, dim=2)) - want) <= (2.0 ** -18 + (d + 272) * 2.0 ** -24) * A).all()
     got = f64(pool)
     assert (abs(got[[3, 1]] - S) <= 2.0 ** -17 * SA).all() and not got[[0, 2]].any()
+
+
+@pytest.mark.parametrize("dtype,d,C,at", [("bf16", 32, 128, 300), ("bf16", 64, 128, 640), ("bf16", 128, 128, 511),
+                                          ("f32", 64, 64, 130)])
+@pytest.mark.parametrize("where,value", [("k", float("nan")), ("v", float("nan")), ("v", float("-inf"))])
+def test_a_token_that_is_not_finite_stays_in_its_head(blin, dtype, d, C, at, where, value):
+    """One bad key or value: from its token on the head's outputs (a value: those of its feature) are
+    not finite, the chunks before it, the other features, heads and rows keep their bits."""
+    B, H, N = 2, 3, 700
+    (q, k, v), pool, lg = inputs(B, H, N, d, dtype, seed=13)
+    lg = torch.full_like(lg, -0.001)
+    ref_pool = pool.clone()
+    ref = blin.decay_prefill(q, k, v, lg, state=ref_pool)
+    (k if where == "k" else v)[1, 2, at, 5] = value
+    o = blin.decay_prefill(q, k, v, lg, state=pool)
+    bad = o[1, 2] if where == "k" else o[1, 2, :, 5]
+    assert not torch.isfinite(bad[at:]).any()
+    state = pool[1, 2, 5] if where == "k" else pool[1, 2, :, 5]
+    assert not torch.isfinite(state).any()
+    first = at // C * C
+    assert torch.equal(o[1, 2, :first], ref[1, 2, :first])
+    if where == "v":
+        rest = [f for f in range(d) if f != 5]
+        assert torch.equal(o[1, 2][:, rest], ref[1, 2][:, rest]) and torch.equal(pool[1, 2][:, rest], ref_pool[1, 2][:, rest])
+    for b, h in [(b, h) for b in range(B) for h in range(H) if (b, h) != (1, 2)]:
+        assert torch.equal(o[b, h], ref[b, h]) and torch.equal(pool[b, h], ref_pool[b, h])
+
+
+def test_memory_made_for_a_call_belongs_to_its_stream(blin):
+    """Work queued on the current stream still writes to memory that has been freed there; a call on
+    another stream, which does not wait for it, must not be given that memory."""
+    (q, k, v), _, lg = inputs(1, 2, 4096, 64, "bf16", seed=14)
+    need = blin.decay_workspace_size(1, 2, 4096, 64)
+    assert need > 1 << 16
+    want = blin.decay_prefill(q, k, v, lg)
+    rot = blin.rope(q, grid=(4096, 1, 1), rope_split=(16, 24, 24))
+    x = torch.randn(8192, 8192, device="cuda", dtype=torch.bfloat16)
+    y = torch.empty_like(x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    late = [torch.empty_like(q) for _ in range(4)] + [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for _ in range(30):
+        torch.matmul(x, x, out=y)
+    for t in late:
+        t.fill_(7)
+    del late, t
+    o = blin.decay_prefill(q, k, v, lg, stream=side)
+    r = blin.rope(q, grid=(4096, 1, 1), rope_split=(16, 24, 24), stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(r, rot)

@@ -157,3 +157,15 @@ def test_the_binding_refuses(blin):
         blin.rope(q, grid=(1, 2, 4), **kw)
     with pytest.raises(blin.BlinError, match="SHAPE"):
         blin.rope(q, grid=(1, 2, 3), rope_split=(8, 12, 14))
+
+
+def test_arguments_without_a_truth_value_or_an_address(blin):
+    q = rand((1, 2, 6, 32), "bf16")
+    with pytest.raises(TypeError, match="inverse"):
+        blin.rope(q, grid=(1, 2, 3), rope_split=(8, 12, 12), inverse=np.zeros(2))
+
+    class NoAddress:
+        cuda_stream = "x"
+
+    with pytest.raises(TypeError, match="stream"):
+        blin.rope(q, grid=(1, 2, 3), rope_split=(8, 12, 12), stream=NoAddress())
