@@ -140,11 +140,16 @@ static Split split_prompt(long long heads, int N, int chunk, int resident, const
     return best;
 }
 
+// Blocks of the second launch that an SM holds.
+static int resident(int d, blin_dtype dt) {
+    if (dt == BLIN_BF16) return d == 32 ? 2 : 1;
+    return d == 128 ? F32Cfg<128>::CTAS : d == 64 ? F32Cfg<64>::CTAS : F32Cfg<32>::CTAS;
+}
+
 static Split split_of(int B, int H, int N, int d, blin_dtype dt) {
     const long long heads = (long long)B * H;
-    if (dt == BLIN_BF16) return split_prompt(heads, N, 128, d == 32 ? 2 : 1, {2.0, 0.25, 0.5, 3.0});
-    return split_prompt(heads, N, kF32Chunk, d == 128 ? F32Cfg<128>::CTAS : d == 64 ? F32Cfg<64>::CTAS : F32Cfg<32>::CTAS,
-                        {0.3, 0.05, 0.4, 0.6});
+    if (dt == BLIN_BF16) return split_prompt(heads, N, 128, resident(d, dt), {2.0, 0.25, 0.5, 3.0});
+    return split_prompt(heads, N, kF32Chunk, resident(d, dt), {0.3, 0.05, 0.4, 0.6});
 }
 
 static size_t workspace_of(const Split &sp, int B, int H, int d) {
@@ -229,6 +234,8 @@ blin_status blin_decay_prefill(const void *q, const void *k, const void *v, void
     a.lengths = lengths;
     a.nseg = sp.nseg;
     a.seg = sp.seg;
+    // the order of rows matters where not all blocks start at once
+    a.sorted = lengths != nullptr && B > 1 && B <= kMaxSorted && (long long)B * H * sp.nseg > kSms * resident(d, dt);
     a.ws = static_cast<float *>(workspace);
     if ((a.wd = watchdog_ptr()) == nullptr) return failf(BLIN_ERR_CUDA, "no CUDA device");
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -27,6 +27,7 @@ struct DecayArgs {
     float *S;            // [slots][H][d][d] or NULL
     int slots;
     const int *slot_of;  // [B] or NULL
+    bool sorted;         // blocks take the batch rows longest first (B <= kMaxSorted)
     int nseg, seg;       // segments of a prompt and tokens per segment (whole chunks)
     float *ws;           // nseg > 1: [B*H][nseg][d*d]: the entering state, then local(0 .. nseg - 2)
     int *wd;
@@ -100,6 +101,25 @@ __device__ __forceinline__ int decay_slot(const DecayArgs &a, int b) {
 // Tokens of batch row b.
 __device__ __forceinline__ int decay_len(const DecayArgs &a, int b) {
     return a.lengths ? min(max(__ldg(a.lengths + b), 0), a.N) : a.N;
+}
+
+// The batch row of block run i.  Rows of unequal lengths go longest first, idle ones
+// last, ties by index: blocks start in order of their numbers, and a long row that
+// started last would run on alone (all threads of the block call it).
+constexpr int kMaxSorted = 128;
+__device__ __forceinline__ int decay_row(const DecayArgs &a, int i) {
+    if (!a.sorted) return i;
+    __shared__ int len[kMaxSorted], row;
+    const int t = threadIdx.x;
+    if (t < a.B) len[t] = a.slot_of && __ldg(a.slot_of + t) < 0 ? 0 : decay_len(a, t);
+    __syncthreads();
+    if (t < a.B) {
+        int rank = 0;
+        for (int r = 0; r < a.B; ++r) rank += len[r] > len[t] || (len[r] == len[t] && r < t);
+        if (rank == i) row = t;
+    }
+    __syncthreads();
+    return row;
 }
 
 // Prompts: fp32 in tf32 parts (kern_decay.cuh), bf16 on tcgen05 (kern_decay_tc.cuh).

@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(256, F32Cfg<D>::CTAS) decay_f32_kernel(const D
           *sp = ss + D * PC, *pw = sp + C * PP;  // sw: weighted keys; ss: the entering state; pw[n] = g^n, n <= C
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t2 = 2 * (lane & 3);
     const int per = STATES ? a.nseg - 1 : a.nseg;
-    const int bh = blockIdx.x / per, seg = blockIdx.x - bh * per;
-    const int b = bh / a.H, h = bh - b * a.H;
+    const int run = blockIdx.x / per, seg = blockIdx.x - run * per;
+    const int b = decay_row(a, run / a.H), h = run % a.H, bh = b * a.H + h;
     const int slot = decay_slot(a, b);
     const int L = slot < 0 ? 0 : decay_len(a, b);
     const int begin = seg * a.seg, end = min(begin + a.seg, L);

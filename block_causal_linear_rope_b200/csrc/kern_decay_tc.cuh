@@ -73,7 +73,7 @@ struct DecayTc {
     static constexpr int OFF_PW = OFF_CTRL + 512;  // g^n for n = 0 .. 128, then scale g^{31 - m} for m < 32
     static constexpr int BYTES = OFF_PW + 4 * (132 + 32) + 1024;
     static_assert(8 * NBAR <= 504, "barriers");
-    static_assert(BYTES <= 227 * 1024, "shared memory");
+    static_assert(BYTES + 4 * (kMaxSorted + 4) <= (D == 32 ? 113 : 227) * 1024, "shared memory");  // and decay_row's
     // Warps: XG and TG warpgroups share the scores and the values of a chunk, UW warps hold the state, ZW the
     // outputs (0: the state's do both).  A d = 32 CTA has one warpgroup of each and no ZW, as two CTAs share an
     // SM.  The last warpgroup holds the producer and the MMA threads.
@@ -691,8 +691,8 @@ __global__ void __launch_bounds__(DecayTc<D, STATES>::THREADS, D == 32 ? 2 : 1)
     uint8_t *base = align1024(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = STATES ? a.nseg - 1 : a.nseg;
-    const int bh = blockIdx.x / per, seg = blockIdx.x - bh * per;
-    const int b = bh / a.H, h = bh - b * a.H;
+    const int run = blockIdx.x / per, seg = blockIdx.x - run * per;
+    const int b = decay_row(a, run / a.H), h = run % a.H, bh = b * a.H + h;
     const int slot = decay_slot(a, b);
     const int L = slot < 0 ? 0 : decay_len(a, b);
     const int begin = seg * a.seg, stop = min(begin + a.seg, a.N);

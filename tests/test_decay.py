@@ -378,3 +378,27 @@ def test_memory_made_for_a_call_belongs_to_its_stream(blin):
     r = blin.rope(q, grid=(4096, 1, 1), rope_split=(16, 24, 24), stream=side)
     torch.cuda.synchronize()
     assert torch.equal(o, want) and torch.equal(r, rot)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 32), ("bf16", 64), ("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("B,H", [(90, 7), (128, 4), (129, 4)])
+def test_many_rows_of_unequal_lengths(blin, B, H, d, dtype):
+    """More blocks than run at a time: each row's results whatever order the rows are taken in."""
+    N, P = 140, B + 3
+    (q, k, v), pool, lg = inputs(B, H, N, d, dtype, seed=15, slots=P)
+    rng = np.random.default_rng([16, B, d])
+    L = rng.integers(0, N + 1, B)
+    L[rng.permutation(B)[:9]] = [0, 0, N, N, 64, 64, 64, 1, 128]
+    slots = rng.permutation(P)[:B]
+    slots[rng.permutation(B)[:3]] = -1
+    S0 = f64(pool)
+    o = blin.decay_prefill(q, k, v, lg, state=pool, slots=torch.from_numpy(slots.astype(np.int32)).cuda(),
+                           lengths=torch.from_numpy(L.astype(np.int32)).cuda(), scale=0.25)
+    after = f64(pool)
+    live = slots >= 0
+    assert not o[torch.from_numpy(~live).cuda()].any()
+    S1, SA = check_out(o[torch.from_numpy(live).cuda()], *(f64(x)[live] for x in (q, k, v)), f64(lg), 0.25, dtype,
+                       S0[slots[live]], L[live])
+    assert (abs(after[slots[live]] - S1) <= 2.0 ** -17 * SA).all()
+    idle = sorted(set(range(P)) - set(slots[live].tolist()))
+    assert (after[idle] == S0[idle]).all()
