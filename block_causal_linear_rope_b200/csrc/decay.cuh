@@ -103,23 +103,30 @@ __device__ __forceinline__ int decay_len(const DecayArgs &a, int b) {
     return a.lengths ? min(max(__ldg(a.lengths + b), 0), a.N) : a.N;
 }
 
-// The batch row of block run i.  Rows of unequal lengths go longest first, idle ones
-// last, ties by index: blocks start in order of their numbers, and a long row that
-// started last would run on alone (all threads of the block call it).
-constexpr int kMaxSorted = 128;
-__device__ __forceinline__ int decay_row(const DecayArgs &a, int i) {
-    if (!a.sorted) return i;
-    __shared__ int len[kMaxSorted], row;
+// The batch row that the blocks of run i take (in the launch that makes the outputs;
+// all threads of the block call it).  Rows of unequal lengths go longest first, idle
+// ones last, ties by index: blocks start in the order of their numbers, and a long
+// row that started last would run on alone.
+constexpr int kMaxSorted = 64;
+static __device__ __noinline__ int sorted_row(const int *lengths, const int *slot_of, int B, int N, int i, int *len) {
     const int t = threadIdx.x;
-    if (t < a.B) len[t] = a.slot_of && __ldg(a.slot_of + t) < 0 ? 0 : decay_len(a, t);
+    if (t < B) len[t] = slot_of && __ldg(slot_of + t) < 0 ? 0 : min(max(__ldg(lengths + t), 0), N);
     __syncthreads();
-    if (t < a.B) {
+    if (t < B) {
         int rank = 0;
-        for (int r = 0; r < a.B; ++r) rank += len[r] > len[t] || (len[r] == len[t] && r < t);
-        if (rank == i) row = t;
+        const int own = len[t];
+#pragma unroll 4
+        for (int r = 0; r < B; ++r) rank += len[r] + (r < t) > own;
+        if (rank == i) len[kMaxSorted] = t;
     }
     __syncthreads();
-    return row;
+    return len[kMaxSorted];
+}
+// scratch: kMaxSorted + 1 ints of shared memory that nobody writes before the block's next barrier
+__device__ __forceinline__ int decay_row(const DecayArgs &a, int i, void *scratch) {
+    if (!a.sorted) return i;
+    // the same in every lane, as the compiler then knows too
+    return __shfl_sync(~0u, sorted_row(a.lengths, a.slot_of, a.B, a.N, i, static_cast<int *>(scratch)), 0);
 }
 
 // Prompts: fp32 in tf32 parts (kern_decay.cuh), bf16 on tcgen05 (kern_decay_tc.cuh).

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(256, F32Cfg<D>::CTAS) decay_f32_kernel(const D
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t2 = 2 * (lane & 3);
     const int per = STATES ? a.nseg - 1 : a.nseg;
     const int run = blockIdx.x / per, seg = blockIdx.x - run * per;
-    const int b = decay_row(a, run / a.H), h = run % a.H, bh = b * a.H + h;
+    const int at = run / a.H, h = run - at * a.H, b = STATES ? at : decay_row(a, at, sq), bh = STATES ? run : b * a.H + h;
     const int slot = decay_slot(a, b);
     const int L = slot < 0 ? 0 : decay_len(a, b);
     const int begin = seg * a.seg, end = min(begin + a.seg, L);

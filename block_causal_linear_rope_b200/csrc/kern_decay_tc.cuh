@@ -73,7 +73,7 @@ struct DecayTc {
     static constexpr int OFF_PW = OFF_CTRL + 512;  // g^n for n = 0 .. 128, then scale g^{31 - m} for m < 32
     static constexpr int BYTES = OFF_PW + 4 * (132 + 32) + 1024;
     static_assert(8 * NBAR <= 504, "barriers");
-    static_assert(BYTES + 4 * (kMaxSorted + 4) <= (D == 32 ? 113 : 227) * 1024, "shared memory");  // and decay_row's
+    static_assert(BYTES <= (D == 32 ? 113 : 227) * 1024, "shared memory");
     // Warps: XG and TG warpgroups share the scores and the values of a chunk, UW warps hold the state, ZW the
     // outputs (0: the state's do both).  A d = 32 CTA has one warpgroup of each and no ZW, as two CTAs share an
     // SM.  The last warpgroup holds the producer and the MMA threads.
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(DecayTc<D, STATES>::THREADS, D == 32 ? 2 : 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = STATES ? a.nseg - 1 : a.nseg;
     const int run = blockIdx.x / per, seg = blockIdx.x - run * per;
-    const int b = decay_row(a, run / a.H), h = run % a.H, bh = b * a.H + h;
+    const int at = run / a.H, h = run - at * a.H, b = STATES ? at : decay_row(a, at, base), bh = STATES ? run : b * a.H + h;
     const int slot = decay_slot(a, b);
     const int L = slot < 0 ? 0 : decay_len(a, b);
     const int begin = seg * a.seg, stop = min(begin + a.seg, a.N);
@@ -713,6 +713,7 @@ __global__ void __launch_bounds__(DecayTc<D, STATES>::THREADS, D == 32 ? 2 : 1)
             u.init_barriers();
             ptx::fence_mbar_init();
         }
+        if (a.sorted) ptx::fence_proxy_async_smem();  // decay_row's scratch lies where the first tile lands
         if (tid < 129) pw[tid] = decay_pow(lg, (float)tid);
         else if (tid < 161) pw[132 + tid - 129] = a.scale * decay_pow(lg, (float)(31 - (tid - 129)));
         if (warp == 0) {
