@@ -27,7 +27,7 @@ static cudaError_t launch_prompt(const DecayArgs &a, int states_threads, int sta
     cudaError_t e = cudaSuccess;
     if (a.nseg > 1) {
         if ((e = allow_smem<States>(states_smem)) != cudaSuccess) return e;
-        States<<<(unsigned)(a.B * a.H * (a.nseg - 1)), states_threads, states_smem, s>>>(args..., a);
+        States<<<(unsigned)(a.B * a.H * a.npiece), states_threads, states_smem, s>>>(args..., a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         note_launch();
     }
@@ -106,37 +106,41 @@ using namespace blin;
 
 static bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Segments of a prompt.  A launch runs its units in waves over the SMs, so its
-// time goes as waves x (chunks of a segment + what a unit costs besides); a split
-// prompt has a first launch (states only) with cheaper chunks, and its second
+// Segments of a prompt and their pieces.  A launch runs its units in waves over the
+// SMs, so its time goes as waves x (chunks of a unit + what a unit costs besides); a
+// split prompt has a first launch (states only) with cheaper chunks, and its second
 // one's units add up the states before them.  The split with the smallest sum is
 // taken, from sizes alone.  The costs are in chunks of the path's second launch
 // as measured on a B200: a chunk of 64 fp32 tokens takes about 7 us, one of 128
 // bf16 tokens 2 to 4 us, and a launch and a unit's start a few us either way (4
 // heads of 300 fp32 tokens: 39 us in one piece, 19 in five; 16 heads of 1024 bf16
 // tokens, d = 64: 23 us in one, 21 in four).
-static constexpr int kSms = 148, kMaxSegments = 32;
+static constexpr int kSms = 148, kMaxStates = 32, kMaxPieces = 4;
 struct Split {
-    int nseg, seg;
+    int nseg, seg, npiece, piece;
 };
 struct SplitCosts {
-    double unit, join, chunk1, launch1;  // a unit's start, a state it adds, a chunk and the rest of the first launch
+    double unit, join, chunk1, unit1, launch1;  // a unit's start, a state it adds, a chunk, a unit's start and the rest of the first launch
 };
 static Split split_prompt(long long heads, int N, int chunk, int resident, const SplitCosts &k) {
     const int nc = std::max(1, (N + chunk - 1) / chunk);
     const long long slots = (long long)kSms * resident;
-    Split best{1, nc * chunk};
-    double cost = 0;
-    for (int s = 1; s <= std::min(nc, kMaxSegments); ++s) {
-        const int len = (nc + s - 1) / s, n = (nc + len - 1) / len;
-        if (n != s || heads * n >= (1LL << 31)) continue;
-        const double waves = (double)((heads * n + slots - 1) / slots), first = (double)((heads * (n - 1) + slots - 1) / slots);
-        const double t = waves * (len + k.unit + k.join * (n - 1)) + first * (k.chunk1 * len + k.launch1);
-        if (s == 1 || t < cost) {
-            cost = t;
-            best = Split{n, len * chunk};
+    const auto waves = [&](long long units) { return (double)((units + slots - 1) / slots); };
+    Split best{1, nc * chunk, 0, nc * chunk};
+    double cost = waves(heads) * (nc + k.unit);
+    for (int s = 2; s <= std::min(nc, kMaxStates); ++s)
+        for (int m = 1; m <= kMaxPieces && (s - 1) * m < kMaxStates; ++m) {
+            const int plen = (nc + s * m - 1) / (s * m), len = plen * m, n = (nc + len - 1) / len;
+            if (n != s || heads * n * m >= (1LL << 31)) continue;
+            const int pieces = (n - 1) * m;
+            const double t = waves(heads * n) * (len + k.unit + k.join * pieces) +
+                             waves(heads * pieces) * (k.chunk1 * plen + k.unit1) + k.launch1;
+            if (t < cost) {
+                cost = t;
+                best = Split{n, len * chunk, pieces, plen * chunk};
+            }
+            if (heads * pieces >= 4 * slots) break;
         }
-    }
     return best;
 }
 
@@ -148,12 +152,12 @@ static int resident(int d, blin_dtype dt) {
 
 static Split split_of(int B, int H, int N, int d, blin_dtype dt) {
     const long long heads = (long long)B * H;
-    if (dt == BLIN_BF16) return split_prompt(heads, N, 128, resident(d, dt), {2.0, 0.25, 0.5, 3.0});
-    return split_prompt(heads, N, kF32Chunk, resident(d, dt), {0.3, 0.05, 0.4, 0.6});
+    if (dt == BLIN_BF16) return split_prompt(heads, N, 128, resident(d, dt), {2.0, 0.25, d == 128 ? 0.67 : 0.5, 1.5, 1.5});
+    return split_prompt(heads, N, kF32Chunk, resident(d, dt), {0.3, 0.05, 0.4, 0.3, 0.3});
 }
 
 static size_t workspace_of(const Split &sp, int B, int H, int d) {
-    return sp.nseg > 1 ? sizeof(float) * (size_t)B * H * sp.nseg * d * d : 16;
+    return sp.nseg > 1 ? sizeof(float) * (size_t)B * H * (1 + sp.npiece) * d * d : 16;
 }
 
 static blin_status check_shape(int B, int H, int N, int d, blin_dtype dt) {
@@ -234,6 +238,8 @@ blin_status blin_decay_prefill(const void *q, const void *k, const void *v, void
     a.lengths = lengths;
     a.nseg = sp.nseg;
     a.seg = sp.seg;
+    a.npiece = sp.npiece;
+    a.piece = sp.piece;
     // the order of rows matters where not all blocks start at once
     a.sorted = lengths != nullptr && B > 1 && B <= kMaxSorted && (long long)B * H * sp.nseg > kSms * resident(d, dt);
     a.ws = static_cast<float *>(workspace);

@@ -3,10 +3,11 @@
 //
 // A prompt is cut into `nseg` segments of whole chunks.  With one segment a CTA
 // walks a head's prompt from its cached state to its end.  With more, a first
-// launch reduces every segment but the last to its local state (what its tokens
-// add to a zero state), and a second one walks the segments side by side, each
-// from the sum of the states before it:
-//   S_in(s) = g^{start_s} S_0 + sum_{s' < s} g^{start_s - end_s'} local(s').
+// launch reduces every segment but the last, in pieces of one or several to a
+// segment, to their local states (what a piece's tokens add to a zero state), and a
+// second one walks the segments side by side, each from the sum of the states
+// before it:
+//   S_in(s) = g^{start_s} S_0 + sum over the pieces p before it of g^{start_s - end_p} local(p).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -29,7 +30,8 @@ struct DecayArgs {
     const int *slot_of;  // [B] or NULL
     bool sorted;         // blocks take the batch rows longest first (B <= kMaxSorted)
     int nseg, seg;       // segments of a prompt and tokens per segment (whole chunks)
-    float *ws;           // nseg > 1: [B*H][nseg][d*d]: the entering state, then local(0 .. nseg - 2)
+    int npiece, piece;   // nseg > 1: pieces of all segments but the last and tokens per piece (whole chunks)
+    float *ws;           // nseg > 1: [B*H][1 + npiece][d*d]: the entering state, then the pieces' local states
     int *wd;
 };
 

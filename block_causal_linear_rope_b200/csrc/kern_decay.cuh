@@ -97,14 +97,14 @@ __global__ void __launch_bounds__(256, F32Cfg<D>::CTAS) decay_f32_kernel(const D
     float *sq = reinterpret_cast<float *>(smem4), *sk = sq + C * PR, *sv = sk + C * PR, *sw = sv + C * PC, *ss = sw + C * PC,
           *sp = ss + D * PC, *pw = sp + C * PP;  // sw: weighted keys; ss: the entering state; pw[n] = g^n, n <= C
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t2 = 2 * (lane & 3);
-    const int per = STATES ? a.nseg - 1 : a.nseg;
+    const int per = STATES ? a.npiece : a.nseg, span = STATES ? a.piece : a.seg;
     const int run = blockIdx.x / per, seg = blockIdx.x - run * per;
     const int at = run / a.H, h = run - at * a.H, b = STATES ? at : decay_row(a, at, sq), bh = STATES ? run : b * a.H + h;
     const int slot = decay_slot(a, b);
     const int L = slot < 0 ? 0 : decay_len(a, b);
-    const int begin = seg * a.seg, end = min(begin + a.seg, L);
+    const int begin = seg * span, end = min(begin + span, L);
     const float lg = decay_log(a.log_decay, h);
-    float *wsp = a.ws + (size_t)bh * a.nseg * D * D;
+    float *wsp = a.ws + (size_t)bh * (1 + a.npiece) * D * D;
     float *pool = a.S && slot >= 0 ? a.S + ((size_t)slot * a.H + h) * D * D : nullptr;
     if (tid <= C) pw[tid] = decay_pow(lg, (float)tid);
     // this warp's part of the state: element (m, n, i) is row srow + 16 m + 8 (i >> 1), column scol + 8 n + (i & 1)
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(256, F32Cfg<D>::CTAS) decay_f32_kernel(const D
             });
         };
         if (a.nseg > 1)
-            for (int s = 0; s <= seg; ++s) add(wsp + (size_t)s * D * D, decay_pow(lg, (float)(begin - s * a.seg)));
+            for (int p = 0; p * a.piece <= begin; ++p) add(wsp + (size_t)p * D * D, decay_pow(lg, (float)(begin - p * a.piece)));
         else if (pool) add(pool, 1.f);
     }
     const float *qp = static_cast<const float *>(a.q) + b * a.lq.batch + h * a.lq.head;

@@ -494,7 +494,7 @@ struct DecayUnit {
 #pragma unroll
         for (int i = 0; i < Cf::NCOL; ++i) st[i] = 0.f;
         if (a.nseg > 1)
-            for (int s = 0; s <= seg; ++s) add(wsp + (size_t)s * D * D, decay_pow(lg, (float)(begin - s * a.seg)));
+            for (int p = 0; p * a.piece <= begin; ++p) add(wsp + (size_t)p * D * D, decay_pow(lg, (float)(begin - p * a.piece)));
         else if (pool) add(pool, 1.f);
     }
     __device__ static void store_state(const float (&st)[Cf::NCOL], float *dst, const Piece &pc, int lane) {
@@ -690,14 +690,14 @@ __global__ void __launch_bounds__(DecayTc<D, STATES>::THREADS, D == 32 ? 2 : 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = align1024(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int per = STATES ? a.nseg - 1 : a.nseg;
+    const int per = STATES ? a.npiece : a.nseg, span = STATES ? a.piece : a.seg;
     const int run = blockIdx.x / per, seg = blockIdx.x - run * per;
     const int at = run / a.H, h = run - at * a.H, b = STATES ? at : decay_row(a, at, base), bh = STATES ? run : b * a.H + h;
     const int slot = decay_slot(a, b);
     const int L = slot < 0 ? 0 : decay_len(a, b);
-    const int begin = seg * a.seg, stop = min(begin + a.seg, a.N);
+    const int begin = seg * span, stop = min(begin + span, a.N);
     float *pool = a.S && slot >= 0 ? a.S + ((size_t)slot * a.H + h) * D * D : nullptr;
-    float *wsp = a.ws + (size_t)bh * a.nseg * D * D;
+    float *wsp = a.ws + (size_t)bh * (1 + a.npiece) * D * D;
     if (STATES && seg == 0)  // the second launch may overwrite the pool while others still read the entering state
         for (int i = tid; i < D * D / 4; i += Cf::THREADS)
             reinterpret_cast<float4 *>(wsp)[i] =
