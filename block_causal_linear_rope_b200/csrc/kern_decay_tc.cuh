@@ -435,14 +435,19 @@ struct DecayUnit {
     __device__ static void split(uint32_t x, float w, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
         float2 v = mul2(x << 16, x & 0xFFFF0000u, make_float2(w, w));
         hi = upper(v);
-        v = rest(v);
+        v = less(v, hi);
         mid = upper(v);
-        lo = upper(rest(v));
+        lo = upper(less(v, mid));
     }
     __device__ static uint32_t upper(float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); }
-    __device__ static float2 rest(float2 v) {
-        return fma2(make_float2(__uint_as_float(__float_as_uint(v.x) & 0xFFFF0000u), __uint_as_float(__float_as_uint(v.y) & 0xFFFF0000u)),
-                    make_float2(-1.f, -1.f), v);
+    // v minus a pair of bf16, by multiply-adds that take them as they are
+    __device__ static float2 less(float2 v, uint32_t h) {
+        float2 r;
+        asm("{\n\t.reg .b16 x, y, m;\n\tmov.b32 {x, y}, %4;\n\tmov.b16 m, 0xBF80;\n\t"
+            "fma.rn.f32.bf16 %0, x, m, %2;\n\tfma.rn.f32.bf16 %1, y, m, %3;\n\t}\n"
+            : "=f"(r.x), "=f"(r.y)
+            : "f"(v.x), "f"(v.y), "r"(h));
+        return r;
     }
     // two multiply-adds in one instruction
     __device__ static float2 fma2(float2 x, float2 y, float2 z) {
@@ -510,7 +515,8 @@ struct DecayUnit {
     // this thread's part of the state as two bf16 operand images, the rounded state and the rounded rest
     __device__ static void put_state(const float (&st)[Cf::NCOL], uint8_t *img, const Piece &pc, int lane) {
         auto low = [](float x, float y, uint32_t hi) {
-            return pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+            const float2 r = less(make_float2(x, y), hi);
+            return pack_bf16x2(r.x, r.y);
         };
         if constexpr (D == 128) {
 #pragma unroll
