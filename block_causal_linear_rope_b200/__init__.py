@@ -637,7 +637,11 @@ def decay_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: 
     in (updated in place; None: start from zero, keep nothing).  `slots`, int32 [B], names each
     row's slot (None: row b uses slot b); a negative entry marks an idle row, whose outputs are
     zeros.  `lengths`, int32 [B], gives each row's tokens (None: all N); outputs past them are
-    zeros."""
+    zeros, and what q, k and v hold there is not used.  An infinity or NaN in a given token makes
+    what follows it in its head not finite, and may reach earlier rows of its chunk of 128 tokens
+    (64 in float32).  `workspace` is scratch of decay_workspace_size() bytes (None: allocated);
+    calls that may run at the same time need separate ones.  With `stream` the call runs there and
+    waits for nothing: what it reads must be ready on that stream."""
     return _result(_ext.decay_prefill(q, k, v, log_decay, state, slots, lengths, scale, out, workspace, _handle(stream)))
 
 

@@ -31,13 +31,13 @@
 // head per CTA: the state then never leaves the registers, and K, V, Q and O
 // cross the memory once.
 //
-// Measured on a B200, sustained: 4 x 32 heads of 32760 tokens, d = 64: 598 us
-// (3.6 TB/s); 32 heads of 32768, d = 128: 506 us; 70 heads of 32760, d = 32:
-// 242 us.  What bounds it: a chunk takes 3300 cycles of an SM at d = 64 (6500 at
-// d = 128, 3600 for two CTAs at d = 32), the round of score product, weights and
+// Measured on a B200, sustained: 4 x 32 heads of 32760 tokens, d = 64: 577 us
+// (3.7 TB/s); 32 heads of 32768, d = 128: 468 us; 70 heads of 32760, d = 32:
+// 241 us.  What bounds it: a chunk takes 3700 cycles of an SM at d = 64 (about 8000
+// at d = 128, 3600 for two CTAs at d = 32), the round of score product, weights and
 // value product that one score buffer allows (two made each chunk's tiles stay
-// longer in the landing ring and were slower, 528 against 511 us), at 41% tensor
-// and 47% issue utilisation; and the card's power: it runs at its 1000 W limit at
+// longer in the landing ring and were slower, 528 against 511 us), at 43% tensor
+// and 42 to 49% issue utilisation; and the card's power: it runs at its 1000 W limit at
 // 1.55 to 1.75 GHz (a plain copy of random data alone takes 997 W at 6.4 TB/s),
 // so that less work per chunk shows as a higher clock, not as fewer cycles.  M =
 // 64 state products at d <= 64 (d = 32 repeats its 32 features by a leading byte
