@@ -402,3 +402,40 @@ def test_many_rows_of_unequal_lengths(blin, B, H, d, dtype):
     assert (abs(after[slots[live]] - S1) <= 2.0 ** -17 * SA).all()
     idle = sorted(set(range(P)) - set(slots[live].tolist()))
     assert (after[idle] == S0[idle]).all()
+
+
+def test_calls_at_the_same_time_and_on_a_forked_stream_of_a_capture(blin):
+    """Split prompts on two streams at once, eager and as two branches of one graph: each has its own
+    scratch, and the bits are those of calls one after the other."""
+    (q, k, v), pool, lg = inputs(2, 2, 5000, 64, "bf16", seed=17)
+    assert blin.decay_workspace_size(2, 2, 5000, 64) > 16
+    lg = torch.full_like(lg, -0.01)
+    halves = [[x[b:b + 1] for x in (q, k, v)] for b in range(2)]
+    start = [pool[b:b + 1].clone() for b in range(2)]
+    ref_pool = [p.clone() for p in start]
+    ref = [blin.decay_prefill(*halves[b], lg, state=ref_pool[b]) for b in range(2)]
+    side = torch.cuda.Stream()
+
+    def both(pools):
+        cur = torch.cuda.current_stream()
+        side.wait_stream(cur)
+        outs = [blin.decay_prefill(*halves[0], lg, state=pools[0]), blin.decay_prefill(*halves[1], lg, state=pools[1], stream=side)]
+        cur.wait_stream(side)
+        return outs
+
+    for _ in range(3):
+        pools = [p.clone() for p in start]
+        outs = both(pools)
+        for b in range(2):
+            assert torch.equal(outs[b], ref[b]) and torch.equal(pools[b], ref_pool[b])
+    static = [p.clone() for p in start]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = both(static)
+    for _ in range(2):
+        for b in range(2):
+            static[b].copy_(start[b])
+        g.replay()
+        for b in range(2):
+            assert torch.equal(outs[b], ref[b]) and torch.equal(static[b], ref_pool[b])
