@@ -67,7 +67,13 @@ struct DecayTc {
     static constexpr int VSUB = IT * ROWB, VPART = NAT * VSUB, VITEM = 3 * VPART;
     static constexpr int SIMG = 2 * D * D;  // a bf16 state image; there are two, high and low part
     static constexpr int OSTG = STATES || D == 128 ? 0 : TILE;      // output staging (d = 128: in the chunk's Q slot)
-    static constexpr int OFF_V = NSLOT * TILE, OFF_S = OFF_V + NVB * VITEM, OFF_O = OFF_S + (STATES ? 0 : 2 * SIMG);
+    // TMEM columns: scores / P, inner and carried outputs, state product.  The three parts of the values
+    // multiply side by side where there is room for a column range each (KVN = 3), else the low part is
+    // added to the middle one's (2), or all to one (1).
+    static constexpr int KVN = D == 128 ? 1 : D == 64 || STATES ? 3 : 2, KVC = KVN * D;
+    static constexpr int ZTILE = KVN == 2 ? 16 * ROWB : 0;  // 16 rows of zeros in front of the weighted values
+    static constexpr int OFF_Z = NSLOT * TILE, OFF_V = OFF_Z + ZTILE, OFF_S = OFF_V + NVB * VITEM,
+                         OFF_O = OFF_S + (STATES ? 0 : 2 * SIMG);
     static constexpr int OFF_CTRL = OFF_O + OSTG;
     static constexpr int NBAR = 2 * NSLOT + 2 * NVB + 13;
     static constexpr int OFF_PW = OFF_CTRL + 512;  // g^n for n = 0 .. 128, then scale g^{31 - m} for m < 32
@@ -82,10 +88,6 @@ struct DecayTc {
     static constexpr int XW = 4 * XG, TW = 4 * TG, ZW = STATES || D == 32 ? 0 : 4, OW = ZW ? ZW : UW;
     static constexpr int THREADS = 32 * (XW + TW + UW + ZW + 4);
     static constexpr int SHARE = 16, RELEASE = SHARE + 1;  // arrivals that free a landing slot
-    // TMEM columns: scores / P, inner and carried outputs, state product.  The three parts of the values
-    // multiply side by side where there is room for a column range each (KVN = 3), else the low part is
-    // added to the middle one's (2), or all to one (1).
-    static constexpr int KVN = D == 128 ? 1 : D == 64 || STATES ? 3 : 2, KVC = KVN * D;
     static constexpr int KB = STATES ? 2 : 1;  // state products in TMEM
     static constexpr int KVM = D == 128 ? 128 : 64;  // rows of the state product
     static constexpr int T_OA = 128, T_OI = T_OA + D, T_KV = STATES ? 0 : T_OI + D;
@@ -215,6 +217,8 @@ struct DecayUnit {
         }
         __device__ Operand(uint32_t l, uint32_t h, int) : lo(l), hi(h) {}
         __device__ Operand operator+(uint32_t bytes) const { return Operand(lo + (bytes >> 4), hi, 0); }
+        // the atoms behind the first one moved by `bytes`
+        __device__ Operand right(uint32_t bytes) const { return Operand(lo + (bytes >> 4 << 16), hi, 0); }
     };
     __device__ static Operand kmajor(uint32_t addr) { return Operand(addr, 16); }
     __device__ static Operand mnmajor(uint32_t addr, uint32_t atom) { return Operand(addr, atom); }
@@ -263,10 +267,14 @@ struct DecayUnit {
         }
         drain();
     }
-    // state product, item by item
+    // State product, item by item.  Products that add to the same columns must all have one shape: only then
+    // does the order in which they were issued hold.  With KVN = 2 the low part therefore goes out as the
+    // right half of a product as wide as that of the two others, with zeros for its left half.
     __device__ void mma_states() const {
         const int nc = chunks();
         const Operand v0 = mnmajor(ptx::smem_u32(vbuf(0)), Cf::VSUB);
+        const uint32_t zeros = ptx::smem_u32(base + Cf::OFF_Z);
+        const Operand low0 = mnmajor(zeros, ptx::smem_u32(vbuf(0)) + 2 * Cf::VPART - zeros);
         static_assert(Cf::NIT % Cf::NVB == 0, "an item's buffer is known at compile time");
         bool ok = true;
         for (int c = 0; c < nc && ok; ++c) {
@@ -292,7 +300,7 @@ struct DecayUnit {
                     } else {
                         if (it == 0 && kk == 0) mma<ID, false>(to, k, v);
                         else mma<ID, true>(to, k, v);
-                        if constexpr (Cf::KVN == 2) mma<ID1, true>(to + D, k, v + 2 * Cf::VPART);
+                        if constexpr (Cf::KVN == 2) mma<ID, true>(to, k, low0.right(it % NB * Cf::VITEM + rstep(kk)));
                     }
                 }
                 ptx::mma_commit(vfree(it % NB));
@@ -719,7 +727,9 @@ __global__ void __launch_bounds__(DecayTc<D, STATES>::THREADS, D == 32 ? 2 : 1)
             u.init_barriers();
             ptx::fence_mbar_init();
         }
-        if (a.sorted) ptx::fence_proxy_async_smem();  // decay_row's scratch lies where the first tile lands
+        if (tid < Cf::ZTILE / 16) reinterpret_cast<uint4 *>(base + Cf::OFF_Z)[tid] = make_uint4(0, 0, 0, 0);
+        // decay_row's scratch lies where the first tile lands; the zeros are read by products
+        if (a.sorted || Cf::ZTILE) ptx::fence_proxy_async_smem();
         if (tid < 129) pw[tid] = decay_pow(lg, (float)tid);
         else if (tid < 161) pw[132 + tid - 129] = a.scale * decay_pow(lg, (float)(31 - (tid - 129)));
         if (warp == 0) {
