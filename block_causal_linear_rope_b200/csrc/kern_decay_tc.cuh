@@ -93,6 +93,10 @@ struct DecayTc {
     static constexpr int T_OA = 128, T_OI = T_OA + D, T_KV = STATES ? 0 : T_OI + D;
     static constexpr int TCOLS = D == 32 ? 256 : STATES && D == 128 ? 256 : 512;
     static_assert(T_KV + KB * KVC <= TCOLS, "TMEM columns");
+    // P: 8 columns for 16 of its own, in 64 free columns where there are (d = 64), else each in the first half
+    // of the scores' columns that it was made of.
+    static constexpr bool POWN = !STATES && TCOLS - (T_KV + KB * KVC) >= 64;
+    static constexpr int T_P = POWN ? T_KV + KB * KVC : 0, PSTEP = POWN ? 8 : 16;
     static constexpr int NCOL = D == 128 ? 64 : D * D / 128;  // state columns per thread
     // With many warps the kernel is launched with RL registers a thread, and the warpgroups that hold the state
     // or the outputs draw on what the others give up.
@@ -239,7 +243,10 @@ struct DecayUnit {
             // a chunk with rows past the prompt's end: once those are cleared
             if (tokens(c) < Cf::C && !wait(one(B_CLEAN), 0, WD_DC_VALUE)) break;
             const Operand qd = kmajor(ptx::smem_u32(slot(tq(c)))), kd = kmajor(ptx::smem_u32(slot(tk(c))));
-            // the scores' columns were last read by the PV product that this thread issued before
+            // The scores' columns were last read by the score warps (B_PREADY).  Where P lies in them, the product
+            // with the values reads it there: that product has another shape and another accumulator, so that
+            // its place in the order of issue does not keep it ahead of this one.
+            if (!Cf::POWN && c > 0 && !wait(ofull(c - 1), (c - 1) >> 1, WD_DC_OUT)) break;
             constexpr uint32_t IDS = ptx::idesc_bf16_f32(128, 128, 0, 0), IDO = ptx::idesc_bf16_f32(128, D, 0, 1);
             mma<IDS, false>(tmem, qd, kd);
 #pragma unroll
@@ -261,7 +268,7 @@ struct DecayUnit {
 #pragma unroll
             for (int kk = 0; kk < Cf::C / 16; ++kk) {
                 const Operand v = vd + rstep(kk);
-                ptx::mma_bf16_ts(tmem + Cf::T_OA, tmem + 16 * kk, v.lo, v.hi, IDO, kk > 0);
+                ptx::mma_bf16_ts(tmem + Cf::T_OA, tmem + Cf::T_P + Cf::PSTEP * kk, v.lo, v.hi, IDO, kk > 0);
             }
             ptx::mma_commit(ofull(c));
         }
@@ -317,14 +324,14 @@ struct DecayUnit {
     }
 
     // ------------------------------------------------------------ score warps (row i per thread)
-    // Columns go in groups of 16, which the XG warps of a row take in turn; a group's P (16 bf16) goes over
-    // the first half of its own columns.  The weights scale g^{i-j} of the diagonal block stay in registers
+    // Columns go in groups of 16, which the XG warps of a row take in turn; a group's P is 16 bf16 in 8
+    // columns.  The weights scale g^{i-j} of the diagonal block stay in registers
     // (0 right of the diagonal); left of it they are g^{i - 32 blk - 31} * scale g^{31 - (j - 32 blk)}, both
     // powers >= 0.
     __device__ void scores(int xw, int lane) const {
         constexpr int XG = Cf::XG == 2 ? 2 : 1, GS = 2 / XG;  // groups of a 32-column block that this warp takes
         const int w = xw & 3, x0 = xw >> 2;
-        const uint32_t row = tmem + (static_cast<uint32_t>(32 * w) << 16);
+        const uint32_t row = tmem + (static_cast<uint32_t>(32 * w) << 16), to = row + Cf::T_P;
         float dw[16 * GS];
 #pragma unroll
         for (int m = 0; m < 16 * GS; ++m) dw[m] = 16 * x0 + m <= lane ? a.scale * pw[lane - m - 16 * x0] : 0.f;
@@ -348,13 +355,13 @@ struct DecayUnit {
                     p[m / 2] = pack_bf16x2(x.x, x.y);
                     p[m / 2 + 1] = pack_bf16x2(y.x, y.y);
                 }
-                ptx::tmem_st(row + 16 * g, p);
+                ptx::tmem_st(to + Cf::PSTEP * g, p);
             }
 #pragma unroll
             for (int g = 0; g < GS; ++g) {
                 uint32_t s[16], p[8];
-                const uint32_t col = row + 32 * w + 16 * (x0 + g);
-                ptx::tmem_ld(col, s);
+                const int gd = 2 * w + x0 + g;
+                ptx::tmem_ld(row + 16 * gd, s);
                 ptx::tmem_wait_ld();
                 ptx::tmem_pin(s);
 #pragma unroll
@@ -362,11 +369,11 @@ struct DecayUnit {
                     const float2 x = mul2(s[m], s[m + 1], make_float2(dw[16 * g + m], dw[16 * g + m + 1]));
                     p[m / 2] = pack_bf16x2(x.x, x.y);
                 }
-                ptx::tmem_st(col, p);
+                ptx::tmem_st(to + Cf::PSTEP * gd, p);
             }
             const uint32_t zero[8] = {};
 #pragma unroll 1
-            for (int g = 2 * w + 2 + x0; g < 8; g += XG) ptx::tmem_st(row + 16 * g, zero);
+            for (int g = 2 * w + 2 + x0; g < 8; g += XG) ptx::tmem_st(to + Cf::PSTEP * g, zero);
             ptx::tmem_wait_st();
             ptx::tc_fence_before_sync();
             warp_arrive(one(B_PREADY), lane);
