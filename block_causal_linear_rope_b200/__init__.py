@@ -10,13 +10,15 @@ library's CUDA kernels.  PyTorch supplies device memory and the current stream.
     o_b = blin.block_step(q_b, k_b, v_b, Hg, Wg, frames=3, rope_split=(8, 12, 12), state=st)
 
 Tensors are contiguous [B, H, N, d] (d = 32 or 64) in float32 or bfloat16 on
-the current CUDA device.  If the library is missing this import raises: there
-is no fallback.
+the current CUDA device.  If the library is missing this import raises, and if
+the extension next to it is, the calls that need it do: there is no fallback.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import re
+import sys
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -132,7 +134,36 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
-from . import _blin_torch as _ext  # noqa: E402  (built next to the library; links it)
+
+
+class _NoExtension:
+    """Stands for the extension that cannot be loaded: each of its functions raises."""
+
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(self._why)
+
+
+def _load_ext():
+    """The extension of decay_prefill, decay_step and rope, built next to the library.  The other calls
+    do not need it, so a missing or unsuitable one is an error of these three only."""
+    path = os.path.join(_PKG, "_blin_torch.so")
+    rebuild = "build it with `python block_causal_linear_rope_b200/build.py` (g++ and torch's headers)"
+    if not os.path.exists(path):
+        return _NoExtension(f"{path} is missing: {rebuild}")
+    try:
+        from . import _blin_torch as ext
+    except ImportError as e:  # unresolved symbols: of another torch or Python, or of an older library
+        return _NoExtension(f"{path} does not load ({e}): {rebuild}")
+    have = "torch {}, Python {}.{}".format(re.match(r"[\d.]*\d", torch.__version__)[0], *sys.version_info)
+    if ext.built_for != have:
+        return _NoExtension(f"{path} was built for {ext.built_for}, but this is {have}: {rebuild}")
+    return ext
+
+
+_ext = _load_ext()
 
 
 def _check(status: int) -> None:

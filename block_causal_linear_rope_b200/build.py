@@ -18,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libblin.so")
 EXT = os.path.join(PKG, "_blin_torch.so")  # tensor-side marshalling (links libblin.so and torch)
 EXT_SRC = os.path.join(CSRC, "blin_torch.cpp")
+EXT_FOR = os.path.join(CSRC, "_build", "blin_torch.for")  # the torch and Python that it was built for
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 SOURCES = ["blin_api.cu", "blin_kernels.cu", "blin_noalloc.cu", "blin_tconv.cu", "blin_decay.cu",
@@ -37,12 +38,14 @@ def _inputs():
 
 def build_ext(force: bool = False) -> str:
     """The CPython extension that checks tensors and calls the library."""
-    srcs = [EXT_SRC, os.path.join(ROOT, "include", "blin.h")]
-    if not force and os.path.exists(EXT) and all(os.path.getmtime(p) <= os.path.getmtime(EXT) for p in srcs):
-        return EXT
     import sysconfig
 
     import torch
+    srcs = [EXT_SRC, os.path.join(ROOT, "include", "blin.h")]
+    now = f"torch {torch.__version__} at {os.path.dirname(torch.__file__)}, Python {sys.version}"
+    if not force and os.path.exists(EXT) and all(os.path.getmtime(p) <= os.path.getmtime(EXT) for p in srcs):
+        if os.path.exists(EXT_FOR) and open(EXT_FOR).read() == now:
+            return EXT
     base = os.path.dirname(torch.__file__)
     inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
@@ -54,6 +57,9 @@ def build_ext(force: bool = False) -> str:
         f"-L{PKG}", "-l:libblin.so", f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
         "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"])
     os.replace(tmp, EXT)
+    os.makedirs(os.path.dirname(EXT_FOR), exist_ok=True)
+    with open(EXT_FOR, "w") as f:
+        f.write(now)
     return EXT
 
 

@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <string>
 #include <vector>
@@ -355,4 +356,14 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_blin_torch", "Tensor-side marshal
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__blin_torch() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__blin_torch() {
+    PyObject *m = PyModule_Create(&module);
+    // what it was built with: its calls into torch and Python hold for these versions only
+    const std::string built = std::string("torch ") + TORCH_VERSION + ", Python " + std::to_string(PY_MAJOR_VERSION) + "." +
+                              std::to_string(PY_MINOR_VERSION);
+    if (m != nullptr && PyModule_AddStringConstant(m, "built_for", built.c_str()) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
