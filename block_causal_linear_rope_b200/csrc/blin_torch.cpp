@@ -40,11 +40,13 @@ std::string text(at::IntArrayRef v) {
     return s + (v.size() == 1 ? ",)" : ")");
 }
 
-// A tensor with `dims` dimensions on a GPU, last dimension contiguous.
+// A tensor with `dims` dimensions, each of which the library's ints can hold.
 const Tensor &operand(PyObject *o, const char *name, int64_t dims, const char *shape) {
     if (!THPVariable_Check(o)) type_error(std::string(name) + " must be a CUDA tensor");
     const Tensor &t = THPVariable_Unpack(o);
     if (t.dim() != dims) value_error(std::string(name) + " must be a " + shape + " tensor");
+    for (const int64_t n : t.sizes())
+        if (n > INT32_MAX) value_error(std::string(name) + "'s dimensions must be below 2^31 (got " + text(t.sizes()) + ")");
     return t;
 }
 void same_kind(const Tensor &t, const char *name, at::IntArrayRef shape, const Tensor &as) {

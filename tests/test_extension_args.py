@@ -1,0 +1,25 @@
+"""What the extension of decay_prefill, decay_step and rope refuses, and what it does for its caller: sizes,
+errors, streams, gradients."""
+import pytest
+import torch
+
+import block_causal_linear_rope_b200 as blin
+
+WIDE = 2 ** 32 + 1  # 1 in 32 bits
+
+
+def test_dimensions_beyond_32_bits_are_refused():
+    """A token count, head count or batch whose low 32 bits name a small problem must not run as that one."""
+    x = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
+    for shape in ((1, 1, WIDE, 64), (1, WIDE, 1, 64), (WIDE, 1, 1, 64)):
+        q = x.expand(shape)
+        with pytest.raises(ValueError, match="2\\^31"):
+            blin.rope(q, grid=(1, 1, 1), rope_split=(16, 24, 24), out=q)
+        with pytest.raises(ValueError, match="2\\^31"):
+            blin.rope(x, q, grid=(1, 1, 1), rope_split=(16, 24, 24))
+        with pytest.raises(ValueError, match="2\\^31"):
+            blin.decay_prefill(q, q, q, torch.zeros(1), out=q)
+    for shape in ((1, WIDE, 64), (WIDE, 1, 64)):
+        q = x[0].expand(shape)
+        with pytest.raises(ValueError, match="2\\^31"):
+            blin.decay_step(q, q, q, torch.zeros(1), torch.zeros(1, 1, 64, 64), out=q)
