@@ -211,6 +211,8 @@ struct Call {
                             std::to_string(d) + "] tensor on " + q.device().str());
             pool = static_cast<float *>(state->data_ptr());
             slots = state->size(0);
+            if (slots < 1 || slots > INT32_MAX)  // an empty tensor has no address: it would pass for no state at all
+                value_error("state must hold between 1 and 2^31 - 1 slots (got " + std::to_string(slots) + ")");
         }
         slot_of = static_cast<const int *>(optional(sl, "slots", at::kInt, {B}, q));
     }

@@ -23,3 +23,15 @@ def test_dimensions_beyond_32_bits_are_refused():
         q = x[0].expand(shape)
         with pytest.raises(ValueError, match="2\\^31"):
             blin.decay_step(q, q, q, torch.zeros(1), torch.zeros(1, 1, 64, 64), out=q)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_pool_without_slots_is_refused(dtype):
+    """Not taken for a call that keeps no state."""
+    q = torch.zeros(2, 3, 5, 64, dtype=dtype, device="cuda")
+    lg, pool = torch.zeros(3, device="cuda"), torch.zeros(0, 3, 64, 64, device="cuda")
+    with pytest.raises(ValueError, match="slots"):
+        blin.decay_prefill(q, q, q, lg, state=pool)
+    with pytest.raises(ValueError, match="slots"):
+        blin.decay_step(q[:, :, 0], q[:, :, 0], q[:, :, 0], lg, pool)
