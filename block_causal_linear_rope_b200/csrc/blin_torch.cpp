@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
@@ -168,15 +169,15 @@ void integers(PyObject *o, const char *name, int *to, int n) {
 void expect_args(Py_ssize_t n, Py_ssize_t want) {
     if (n != want) type_error("expected " + std::to_string(want) + " arguments, got " + std::to_string(n));
 }
-// Runs the body; a refusal or a C++ exception becomes a Python one.
+// Runs the body; a refusal or a C++ exception becomes a Python one, torch's own those that torch makes of them.
 template <typename F>
 PyObject *guarded(F &&body) {
     try {
         return body();
     } catch (const Refused &r) {
         PyErr_SetString(r.type, r.what.c_str());
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

@@ -35,3 +35,15 @@ def test_a_pool_without_slots_is_refused(dtype):
         blin.decay_prefill(q, q, q, lg, state=pool)
     with pytest.raises(ValueError, match="slots"):
         blin.decay_step(q[:, :, 0], q[:, :, 0], q[:, :, 0], lg, pool)
+
+
+@pytest.mark.gpu
+def test_no_memory_for_an_output_is_torchs_error():
+    """As of a torch operation: programs that answer it by a smaller batch catch this type."""
+    q = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda").expand(1, 4096, 2 ** 24, 64)  # 8 TiB of output
+    with pytest.raises(torch.OutOfMemoryError):
+        torch.empty(q.shape, dtype=q.dtype, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        blin.rope(q, grid=(2 ** 24, 1, 1), rope_split=(16, 24, 24))
+    with pytest.raises(torch.OutOfMemoryError):
+        blin.decay_prefill(q, q, q, torch.zeros(4096, device="cuda"))
