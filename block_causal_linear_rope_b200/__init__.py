@@ -672,7 +672,8 @@ def decay_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: 
     what follows it in its head not finite, and may reach earlier rows of its chunk of 128 tokens
     (64 in float32).  `workspace` is scratch of decay_workspace_size() bytes (None: allocated);
     calls that may run at the same time need separate ones.  With `stream` the call runs there and
-    waits for nothing: what it reads must be ready on that stream."""
+    waits for nothing: what it reads must be ready on that stream.  There is no gradient: a call
+    that autograd would have to record is refused."""
     return _result(_ext.decay_prefill(q, k, v, log_decay, state, slots, lengths, scale, out, workspace, _handle(stream)))
 
 
@@ -685,6 +686,30 @@ def decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: tor
 
 
 # ----------------------------------------------------------------------------- rotary embedding
+class _Rope(torch.autograd.Function):
+    """rope() where autograd records it: the gradient is the rotation by the negative angles."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, kw, stream):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(positions)
+        ctx.kw = kw
+        r = rope(q, k, positions=positions, stream=stream, **kw)
+        ctx.mark_non_differentiable(*(t for t, need in zip((r,) if k is None else r, ctx.needs_input_grad) if not need))
+        return r
+
+    @staticmethod
+    def backward(ctx, *grads):
+        kw = dict(ctx.kw, inverse=not ctx.kw["inverse"], positions=ctx.saved_tensors[0])
+        g = [None if t is None else t.contiguous() for t in grads]  # a sum's gradient has no strides
+        g = [t if t is None or t.data_ptr() % 16 == 0 else t.clone() for t in g]
+        given = [t for t in g if t is not None]
+        r = rope(*given, **kw) if given else None
+        r = list(r) if len(given) == 2 else [r]
+        g = [None if t is None else r.pop(0) for t in g]
+        return g[0], g[1] if len(g) == 2 else None, None, None, None
+
+
 def rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, rope_split: Sequence[int],
          grid: Optional[Sequence[int]] = None, t0: int = 0, positions: Optional[torch.Tensor] = None,
          theta: float = 1e4, inverse: bool = False, out=None, stream=None):
@@ -693,8 +718,13 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, rope_split: Seque
 
     Positions come from grid=(T, Hg, Wg), N = T*Hg*Wg, with frames counted from t0, or from
     `positions`, int32 [B, N, 3] or [N, 3] (t, y, x) of each token.  rope_split may sum to less
-    than d; features past it are copied.  inverse=True rotates back, which is also the gradient:
-    rope(g, inverse=True) takes an output's gradient to its input's.  `out` is a tensor, or a
-    (q, k) pair of tensors, to write to; an output may be its own input.  Returns q's rotation,
+    than d; features past it are copied.  inverse=True rotates back, which is also the gradient
+    that autograd gets for a q or k that requires one (its backward pass runs on the stream that
+    was current at the call).  `out` is a tensor, or a (q, k) pair of tensors, to write to; an
+    output may be its own input; autograd cannot record a call with `out`.  Returns q's rotation,
     or the pair."""
-    return _result(_ext.rope(q, k, rope_split, grid, t0, positions, theta, inverse, out, _handle(stream)))
+    r = _ext.rope(q, k, rope_split, grid, t0, positions, theta, inverse, out, _handle(stream))
+    if r is NotImplemented:  # a q or k whose gradient is recorded
+        kw = dict(rope_split=tuple(rope_split), grid=grid, t0=t0, theta=theta, inverse=bool(inverse))
+        return _Rope.apply(q, k, positions, kw, stream)
+    return _result(r)

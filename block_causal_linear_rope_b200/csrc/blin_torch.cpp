@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -34,6 +35,7 @@ struct Refused {
 };
 [[noreturn]] void value_error(const std::string &w) { throw Refused{PyExc_ValueError, w}; }
 [[noreturn]] void type_error(const std::string &w) { throw Refused{PyExc_TypeError, w}; }
+[[noreturn]] void runtime_error(const std::string &w) { throw Refused{PyExc_RuntimeError, w}; }
 
 std::string text(at::IntArrayRef v) {
     std::string s = "(";
@@ -80,6 +82,8 @@ const void *optional(PyObject *o, const char *name, at::ScalarType type, at::Int
     value_error(std::string(name) + " must be a contiguous " + at::toString(type) + " tensor of shape " + text(shape) + " on " +
                 as.device().str());
 }
+// Would autograd have to record an operation on this tensor?
+bool recorded(const Tensor &t) { return at::GradMode::is_enabled() && t.requires_grad(); }
 bool same_place(const Tensor &a, const Tensor &b) { return a.const_data_ptr() == b.const_data_ptr() && a.strides() == b.strides(); }
 // An output must not overlap an input: contiguous tensors are compared by address range, strided views,
 // which may interleave without sharing an element, only by start address.
@@ -216,10 +220,16 @@ struct Call {
                 value_error("state must hold between 1 and 2^31 - 1 slots (got " + std::to_string(slots) + ")");
         }
         slot_of = static_cast<const int *>(optional(sl, "slots", at::kInt, {B}, q));
+        if (recorded(q) || recorded(k) || recorded(v) || recorded(THPVariable_Unpack(a[3])) || (state && recorded(*state)))
+            no_gradient();
+    }
+    [[noreturn]] static void no_gradient() {
+        runtime_error("the decayed attention has no gradient: call it under torch.no_grad(), or with tensors that require none");
     }
     Tensor output(PyObject *o, const CallStream &on) const {
         if (o == Py_None) return on.output(q.sizes(), q);
         const Tensor &t = given_out(o, q);
+        if (recorded(t)) no_gradient();
         no_overlap(t, q), no_overlap(t, k), no_overlap(t, v);
         if (state) no_overlap(t, *state);
         return t;
@@ -281,7 +291,8 @@ PyObject *decay_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// q, k, rope_split, grid, t0, positions, theta, inverse, out, stream
+// q, k, rope_split, grid, t0, positions, theta, inverse, out, stream; NotImplemented where autograd has to record
+// the call
 PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         expect_args(n, 10);
@@ -314,6 +325,8 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
             PyErr_Clear();
             type_error("inverse must be True or False");
         }
+        const bool record = recorded(q) || (two && recorded(k));
+        if (record && a[8] == Py_None) Py_RETURN_NOTIMPLEMENTED;
         const CallStream on(a[9], q);
         Tensor out[2];
         const Tensor *in[2] = {&q, &k};
@@ -327,6 +340,8 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
             for (int i = 0; i < outs && seq; ++i) o[i] = PyTuple_Check(a[8]) ? PyTuple_GET_ITEM(a[8], i) : PyList_GET_ITEM(a[8], i);
             for (int i = 0; i < outs; ++i) {
                 out[i] = given_out(o[i], *in[i]);
+                if (record || recorded(out[i]))
+                    runtime_error("rope with out= has no gradient: call it under torch.no_grad(), or with tensors that require none");
                 for (int j = 0; j < outs; ++j)
                     if (i != j || !same_place(out[i], *in[i])) no_overlap(out[i], *in[j]);
             }

@@ -47,3 +47,109 @@ def test_no_memory_for_an_output_is_torchs_error():
         blin.rope(q, grid=(2 ** 24, 1, 1), rope_split=(16, 24, 24))
     with pytest.raises(torch.OutOfMemoryError):
         blin.decay_prefill(q, q, q, torch.zeros(4096, device="cuda"))
+
+
+@pytest.mark.gpu
+def test_the_decayed_attention_refuses_what_autograd_would_record():
+    q, k, v = (torch.randn(2, 3, 5, 64, device="cuda") for _ in range(3))
+    lg, pool = torch.full((3,), -0.1, device="cuda"), torch.zeros(2, 3, 64, 64, device="cuda")
+    one = [x[:, :, 0] for x in (q, k, v)]
+    want, step = blin.decay_prefill(q, k, v, lg), blin.decay_step(*one, lg, pool.clone())
+    for i in range(6):  # q, k, v, log_decay, the pool, out
+        def leaf(j, t):
+            return t.detach().clone().requires_grad_() if i == j else t
+        full = [leaf(j, t) for j, t in enumerate((q, k, v, lg))]
+        last = [leaf(j, t.contiguous()) for j, t in enumerate((*one, lg))]
+        state, out, out1 = leaf(4, pool.clone()), leaf(5, torch.empty_like(q)), leaf(5, torch.empty_like(one[0]))
+        with pytest.raises(RuntimeError, match="gradient"):
+            blin.decay_prefill(*full, state=state, out=out)
+        with pytest.raises(RuntimeError, match="gradient"):
+            blin.decay_step(*last, state, out=out1)
+        for off in (torch.no_grad(), torch.inference_mode()):
+            with off:
+                assert torch.equal(blin.decay_prefill(*full, state=state.clone(), out=out), want)
+                assert torch.equal(blin.decay_step(*last, state.clone(), out=out1), step)
+
+
+SPLIT, GRID = (16, 24, 16), (3, 4, 5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("given", [False, True])
+def test_autograd_records_rope(dtype, inverse, given):
+    """The gradient of a weighted sum of both outputs is the weights rotated back: to the bits, as it is the
+    same kernel; that this is the formula's gradient and the differences' is test_rope's."""
+    B, N, d = 2, 60, 64
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    q, k, gq, gk = (torch.randn(B, h, N, d, generator=gen, device="cuda").to(dtype) for h in (3, 2, 3, 2))
+    kw = dict(rope_split=SPLIT, theta=5e3)
+    if given:
+        kw["positions"] = torch.randint(-9, 9999, (B, N, 3), generator=gen, device="cuda", dtype=torch.int32)
+    else:
+        kw.update(grid=GRID, t0=2)
+    want = blin.rope(q, k, inverse=inverse, **kw)
+    back = blin.rope(gq, gk, inverse=not inverse, **kw)
+    for need in ((True, True), (True, False), (False, True)):
+        x, y = q.clone().requires_grad_(need[0]), k.clone().requires_grad_(need[1])
+        outs = blin.rope(x, y, inverse=inverse, **kw)
+        assert all(torch.equal(o, w) and o.requires_grad == n for o, w, n in zip(outs, want, need))
+        torch.autograd.backward([o for o, n in zip(outs, need) if n], [g for g, n in zip((gq, gk), need) if n])
+        for t, g, n in zip((x, y), back, need):
+            assert torch.equal(t.grad, g) if n else t.grad is None
+    # one output used, by a sum (a gradient without strides); q alone; a second derivative
+    x, y = q.clone().requires_grad_(), k.clone().requires_grad_()
+    a, b = blin.rope(x, y, inverse=inverse, **kw)
+    b.sum().backward()
+    assert x.grad is None and torch.equal(y.grad, blin.rope(torch.ones_like(k), inverse=not inverse, **kw))
+    z = blin.rope(x, inverse=inverse, **kw)
+    (g,) = torch.autograd.grad(z, x, gq.clone().requires_grad_(), create_graph=True)
+    assert torch.equal(z, want[0]) and torch.equal(g, back[0]) and g.requires_grad
+    u = gq.clone().requires_grad_()
+    (g,) = torch.autograd.grad(z, x, u, create_graph=True)
+    (g2,) = torch.autograd.grad(g, u, q)
+    assert torch.equal(g2, want[0])
+
+
+@pytest.mark.gpu
+def test_rope_with_out_refuses_what_autograd_would_record():
+    q, k = (torch.randn(1, 2, 60, 64, device="cuda") for _ in range(2))
+    kw = dict(grid=GRID, rope_split=SPLIT)
+    want = blin.rope(q, k, **kw)
+    x = q.clone().requires_grad_()
+    for args, out in (((x, k), (torch.empty_like(q), torch.empty_like(k))), ((x, k), (x, k)), ((k, x), (k, x)),
+                      ((q, k), (torch.empty_like(q), torch.empty_like(q).requires_grad_()))):
+        with pytest.raises(RuntimeError, match="gradient"):
+            blin.rope(*args, out=out, **kw)
+    assert torch.equal(x, q)
+    with torch.no_grad():
+        got = blin.rope(x, k.clone(), out=(x, torch.empty_like(k)), **kw)
+        assert got[0] is x and torch.equal(x, want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+def test_a_training_step_through_rope_in_a_graph():
+    """Forward and backward captured and replayed: the eager gradients."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    w, x = (torch.randn(1, 2, 60, 64, generator=gen, device="cuda") for _ in range(2))
+
+    def grads(x):
+        q = (x * 2).requires_grad_()
+        a, b = blin.rope(q, q * 0.5, grid=GRID, rope_split=SPLIT)
+        return torch.autograd.grad((a * w).sum() + (b * b * w).sum(), q)[0]
+
+    static = x.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        grads(static)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = grads(static)
+    for seed in (2, 3):
+        new = torch.randn(x.shape, generator=gen, device="cuda")
+        static.copy_(new)
+        g.replay()
+        assert torch.equal(out, grads(new))
