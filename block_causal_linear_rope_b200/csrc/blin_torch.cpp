@@ -84,6 +84,10 @@ const void *optional(PyObject *o, const char *name, at::ScalarType type, at::Int
 }
 // Would autograd have to record an operation on this tensor?
 bool recorded(const Tensor &t) { return at::GradMode::is_enabled() && t.requires_grad(); }
+// Tells autograd that a call has written to a tensor of the caller's.
+void written(const Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 bool same_place(const Tensor &a, const Tensor &b) { return a.const_data_ptr() == b.const_data_ptr() && a.strides() == b.strides(); }
 // An output must not overlap an input: contiguous tensors are compared by address range, strided views,
 // which may interleave without sharing an element, only by start address.
@@ -185,8 +189,6 @@ PyObject *guarded(F &&body) {
     }
     return nullptr;
 }
-PyObject *answer(blin_status rc, const Tensor &out) { return rc == BLIN_OK ? THPVariable_Wrap(out) : PyLong_FromLong(rc); }
-
 // What a prefill and a step share: q, k, v, log_decay, the pool and the slots.
 struct Call {
     const Tensor &q, &k, &v;
@@ -237,6 +239,13 @@ struct Call {
     bool dense(const Tensor &out) const {
         return q.is_contiguous() && k.is_contiguous() && v.is_contiguous() && out.is_contiguous();
     }
+    // The output, or the status of a call that failed.
+    PyObject *answer(blin_status rc, const Tensor &out, PyObject *given) const {
+        if (rc != BLIN_OK) return PyLong_FromLong(rc);
+        if (state) written(*state);
+        if (given != Py_None) written(out);
+        return THPVariable_Wrap(out);
+    }
     blin_decay_layouts layouts(const Tensor &out) const { return {layout(q), layout(k), layout(v), layout(out)}; }
 };
 
@@ -267,11 +276,12 @@ PyObject *decay_prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
             ws_bytes = need;
         }
         const blin_decay_layouts lay = c.layouts(out);
-        return answer(blin_decay_prefill(c.q.const_data_ptr(), c.k.const_data_ptr(), c.v.const_data_ptr(), out.data_ptr(), c.dt,
-                                         (int)c.B, (int)c.H, (int)N, (int)c.d, c.lg, number(a[7], "scale"),
-                                         c.dense(out) ? nullptr : &lay, lengths, c.pool, (int)c.slots, c.slot_of, ws, ws_bytes,
-                                         on.stream()),
-                      out);
+        const blin_status rc =
+            blin_decay_prefill(c.q.const_data_ptr(), c.k.const_data_ptr(), c.v.const_data_ptr(), out.data_ptr(), c.dt, (int)c.B,
+                               (int)c.H, (int)N, (int)c.d, c.lg, number(a[7], "scale"), c.dense(out) ? nullptr : &lay, lengths,
+                               c.pool, (int)c.slots, c.slot_of, ws, ws_bytes, on.stream());
+        if (rc == BLIN_OK && a[9] != Py_None) written(THPVariable_Unpack(a[9]));
+        return c.answer(rc, out, a[8]);
     });
 }
 
@@ -284,10 +294,11 @@ PyObject *decay_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const CallStream on(a[8], c.q);
         const Tensor out = c.output(a[7], on);
         const blin_decay_layouts lay = c.layouts(out);
-        return answer(blin_decay_step(c.q.const_data_ptr(), c.k.const_data_ptr(), c.v.const_data_ptr(), out.data_ptr(), c.dt,
-                                      (int)c.B, (int)c.H, (int)c.d, c.lg, number(a[6], "scale"), c.dense(out) ? nullptr : &lay,
-                                      c.pool, (int)c.slots, c.slot_of, on.stream()),
-                      out);
+        const blin_status rc =
+            blin_decay_step(c.q.const_data_ptr(), c.k.const_data_ptr(), c.v.const_data_ptr(), out.data_ptr(), c.dt, (int)c.B,
+                            (int)c.H, (int)c.d, c.lg, number(a[6], "scale"), c.dense(out) ? nullptr : &lay, c.pool, (int)c.slots,
+                            c.slot_of, on.stream());
+        return c.answer(rc, out, a[7]);
     });
 }
 
@@ -363,7 +374,9 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
             blin_rope(q.const_data_ptr(), out[0].data_ptr(), (int)q.size(1), two ? k.const_data_ptr() : nullptr,
                       two ? out[1].data_ptr() : nullptr, two ? (int)k.size(1) : 0, dt, (int)B, (int)N, (int)d, &g,
                       (int)integer(a[4], "t0"), pos, shared, inverse, dense ? nullptr : &lay, on.stream());
-        return rc == BLIN_OK ? result() : PyLong_FromLong(rc);
+        if (rc != BLIN_OK) return PyLong_FromLong(rc);
+        for (int i = 0; i < outs && a[8] != Py_None; ++i) written(out[i]);
+        return result();
     });
 }
 

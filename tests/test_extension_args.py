@@ -153,3 +153,32 @@ def test_a_training_step_through_rope_in_a_graph():
         static.copy_(new)
         g.replay()
         assert torch.equal(out, grads(new))
+
+
+@pytest.mark.gpu
+def test_autograd_learns_of_tensors_that_were_written_to():
+    """A tensor saved for a backward pass and then overwritten is an error there, not a wrong gradient."""
+    q, k, v = (torch.randn(2, 3, 60, 64, device="cuda") for _ in range(3))
+    lg, pool = torch.full((3,), -0.1, device="cuda"), torch.zeros(2, 3, 64, 64, device="cuda")
+    kw = dict(grid=GRID, rope_split=SPLIT)
+    ws = torch.empty(blin.decay_workspace_size(2, 3, 60, 64, torch.float32), dtype=torch.uint8, device="cuda")
+
+    def writes(call, *to):
+        before = [t._version for t in to]
+        read = [t._version for t in (k, v, lg)]
+        call()
+        assert [t._version for t in to] == [n + 1 for n in before] and [t._version for t in (k, v, lg)] == read
+
+    o, o1, r = torch.empty_like(q), torch.empty_like(q[:, :, 0]), torch.empty_like(q)
+    writes(lambda: blin.decay_prefill(q, k, v, lg, state=pool, out=o, workspace=ws), pool, o, ws)
+    writes(lambda: blin.decay_step(q[:, :, 0], k[:, :, 0], v[:, :, 0], lg, pool, out=o1), pool, o1)
+    writes(lambda: blin.rope(q, k, out=(q, r), **kw), q, r)
+    w = torch.ones_like(q, requires_grad=True)
+    y = (w * q).sum()
+    blin.rope(q, out=q, **kw)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward()
+    with torch.inference_mode():
+        a, p = torch.zeros_like(q), torch.zeros_like(pool)
+        blin.decay_prefill(q, k, v, lg, state=p, out=a)
+    blin.decay_prefill(q, k, v, lg, state=p, out=a)  # tensors of inference mode count no versions
