@@ -672,7 +672,8 @@ def decay_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: 
     what follows it in its head not finite, and may reach earlier rows of its chunk of 128 tokens
     (64 in float32).  `workspace` is scratch of decay_workspace_size() bytes (None: allocated);
     calls that may run at the same time need separate ones.  With `stream` the call runs there and
-    waits for nothing: what it reads must be ready on that stream.  There is no gradient: a call
+    waits for nothing: what it reads must be ready on that stream; the tensors' memory is kept
+    until the call has done with it.  There is no gradient: a call
     that autograd would have to record is refused."""
     return _result(_ext.decay_prefill(q, k, v, log_decay, state, slots, lengths, scale, out, workspace, _handle(stream)))
 

@@ -118,6 +118,8 @@ blin_layout layout(const Tensor &t) {
 // The call's stream: the current one, or the handle that the wrapper hands over.  Memory that the call makes
 // belongs to its stream (the current stream's may still be in use there by work that the call's does not wait
 // for); what it returns is kept until the current stream, where it is most likely read, has also done with it.
+// What the caller hands over is kept until the call's stream has done with it: on its own stream the memory of a
+// tensor that goes out of use right after the call would be given away while the call may still read it.
 class CallStream {
     c10::cuda::CUDAStream current_, used_;
     c10::cuda::OptionalCUDAStreamGuard guard_;
@@ -138,6 +140,12 @@ public:
         if (used_ != current_) guard_.reset_stream(used_);
     }
     cudaStream_t stream() const { return used_.stream(); }
+    void keep(const Tensor &t) const {
+        if (used_ != current_) t.record_stream(used_);
+    }
+    void keep(PyObject *o) const {
+        if (o != Py_None) keep(THPVariable_Unpack(o));
+    }
     Tensor output(at::IntArrayRef shape, const Tensor &like) const {
         Tensor t = at::empty(shape, like.options().memory_format(at::MemoryFormat::Contiguous));
         if (used_ != current_) t.record_stream(current_);
@@ -228,12 +236,17 @@ struct Call {
     [[noreturn]] static void no_gradient() {
         runtime_error("the decayed attention has no gradient: call it under torch.no_grad(), or with tensors that require none");
     }
+    void keep(const CallStream &on, PyObject *lg, PyObject *sl) const {
+        on.keep(q), on.keep(k), on.keep(v), on.keep(lg), on.keep(sl);
+        if (state) on.keep(*state);
+    }
     Tensor output(PyObject *o, const CallStream &on) const {
         if (o == Py_None) return on.output(q.sizes(), q);
         const Tensor &t = given_out(o, q);
         if (recorded(t)) no_gradient();
         no_overlap(t, q), no_overlap(t, k), no_overlap(t, v);
         if (state) no_overlap(t, *state);
+        on.keep(t);
         return t;
     }
     bool dense(const Tensor &out) const {
@@ -257,6 +270,7 @@ PyObject *decay_prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t N = c.q.size(2);
         const int *lengths = static_cast<const int *>(optional(a[6], "lengths", at::kInt, {c.B}, c.q));
         const CallStream on(a[10], c.q);
+        c.keep(on, a[3], a[5]), on.keep(a[6]);
         const Tensor out = c.output(a[8], on);
         if (N == 0 && c.B > 0 && c.H > 0) return THPVariable_Wrap(out);  // no tokens: nothing to read, no address to give
         const size_t need = blin_decay_workspace_size((int)c.B, (int)c.H, (int)N, (int)c.d, c.dt);
@@ -268,6 +282,7 @@ PyObject *decay_prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
             const Tensor &w = THPVariable_Unpack(a[9]);
             if (w.device() != c.q.device() || !w.is_contiguous())
                 value_error("workspace must be a contiguous tensor on " + c.q.device().str());
+            on.keep(w);
             ws = w.data_ptr();
             ws_bytes = w.nbytes();
         } else if (need > 16) {
@@ -292,6 +307,7 @@ PyObject *decay_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Call c(a, 3, "[B, H, d]", a[4], a[5]);
         if (c.state == nullptr) value_error("a step needs a state");
         const CallStream on(a[8], c.q);
+        c.keep(on, a[3], a[5]);
         const Tensor out = c.output(a[7], on);
         const blin_decay_layouts lay = c.layouts(out);
         const blin_status rc =
@@ -339,6 +355,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const bool record = recorded(q) || (two && recorded(k));
         if (record && a[8] == Py_None) Py_RETURN_NOTIMPLEMENTED;
         const CallStream on(a[9], q);
+        on.keep(q), on.keep(k), on.keep(a[5]);
         Tensor out[2];
         const Tensor *in[2] = {&q, &k};
         const int outs = two ? 2 : 1;
@@ -357,6 +374,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
                     if (i != j || !same_place(out[i], *in[i])) no_overlap(out[i], *in[j]);
             }
             if (two) no_overlap(out[0], out[1]);
+            for (int i = 0; i < outs; ++i) on.keep(out[i]);
         }
         if (!two) out[1] = out[0];
         auto result = [&]() -> PyObject * {

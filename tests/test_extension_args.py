@@ -182,3 +182,51 @@ def test_autograd_learns_of_tensors_that_were_written_to():
         a, p = torch.zeros_like(q), torch.zeros_like(pool)
         blin.decay_prefill(q, k, v, lg, state=p, out=a)
     blin.decay_prefill(q, k, v, lg, state=p, out=a)  # tensors of inference mode count no versions
+
+
+@pytest.mark.gpu
+def test_inputs_live_until_the_calls_stream_has_read_them():
+    """A call waits on a busy stream while its caller drops the inputs and the current stream writes to
+    memory of their sizes: the call must still read the inputs."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    B, H, N, d = 2, 4, 4096, 64
+    big = torch.randn(8192, 8192, device="cuda", dtype=torch.bfloat16)
+    y = torch.empty_like(big)
+    side = torch.cuda.Stream()
+    q, k, v = (torch.randn(B, H, N, d, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(3))
+    lg, slots = torch.tensor([-0.1, -0.01, 0.0, -0.5], device="cuda"), torch.tensor([2, 0], dtype=torch.int32, device="cuda")
+    lengths = torch.tensor([N, N - 77], dtype=torch.int32, device="cuda")
+    pos = torch.randint(0, 9999, (B, N, 3), generator=gen, device="cuda", dtype=torch.int32)
+    pool = torch.randn(3, H, d, d, generator=gen, device="cuda")
+    need = blin.decay_workspace_size(B, H, N, d)
+    one = [x[:, :, 3].contiguous() for x in (q, k, v)]
+
+    def prefill(q, k, v, lg, slots, lengths, pool, ws, **kw):
+        return blin.decay_prefill(q, k, v, lg, state=pool, slots=slots, lengths=lengths, workspace=ws, **kw)
+
+    def step(q, k, v, lg, slots, pool, **kw):
+        return blin.decay_step(q, k, v, lg, pool, slots=slots, **kw)
+
+    def rope(q, k, pos, **kw):
+        return torch.cat(blin.rope(q, k, positions=pos, rope_split=SPLIT, **kw)) if not kw else blin.rope(
+            q, k, positions=pos, rope_split=SPLIT, **kw)
+
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert need > 16
+    for call, args in ((prefill, (q, k, v, lg, slots, lengths, pool, ws)), (step, (*one, lg, slots, pool)),
+                       (rope, (q, k, pos))):
+        want = call(*(t.clone() for t in args))
+        for last in (False, True):  # first a run that loads every kernel, which may wait for the device
+            copies = [t.clone() for t in args]
+            torch.cuda.synchronize()
+            with torch.cuda.stream(side):
+                for _ in range(200):  # about a tenth of a second
+                    torch.matmul(big, big, out=y)
+            got = call(*copies, stream=side)
+            del copies
+            late = [torch.empty_like(t).view(torch.uint8).fill_(0xFF) for t in args for _ in range(8)]
+            torch.cuda.current_stream().synchronize()
+            assert not last or not side.query()  # the call had not begun when the memory was written to
+            torch.cuda.synchronize()
+            assert torch.equal(got if torch.is_tensor(got) else torch.cat(got), want)
+            del late
