@@ -85,3 +85,18 @@ def test_the_extension_is_built_again_for_another_torch(tmp_path, monkeypatch):
     assert len(runs) == 2
     build.build_ext(force=True)
     assert len(runs) == 3
+
+
+def test_the_extension_never_reaches_the_oracle():
+    """test_separation looks at the CUDA sources and the library; the same for the C++ source and the extension."""
+    import re
+    csrc = os.path.join(PKG, "csrc")
+    names = [n for n in os.listdir(csrc) if n.endswith((".cpp", ".cc", ".c", ".hpp"))]
+    assert names == ["blin_torch.cpp"]
+    with open(os.path.join(csrc, names[0])) as f:
+        incs = re.findall(r'^\s*#\s*include\s*[<"]([^>"]+)[>"]', f.read(), flags=re.M)
+    assert incs and not any("oracle" in i for i in incs)
+    ext = os.path.join(PKG, "_blin_torch.so")
+    needed = subprocess.run(["readelf", "-d", ext], capture_output=True, text=True).stdout
+    syms = subprocess.run(["nm", "-D", ext], capture_output=True, text=True).stdout
+    assert "libblin.so" in needed and "oracle" not in needed and syms and "oracle" not in syms
