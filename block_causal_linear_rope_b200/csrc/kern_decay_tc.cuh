@@ -246,7 +246,10 @@ struct DecayUnit {
             // The scores' columns were last read by the score warps (B_PREADY).  Where P lies in them, the product
             // with the values reads it there: that product has another shape and another accumulator, so that
             // its place in the order of issue does not keep it ahead of this one.
-            if (!Cf::POWN && c > 0 && !wait(ofull(c - 1), (c - 1) >> 1, WD_DC_OUT)) break;
+            if (!Cf::POWN && c > 0) {
+                if (!wait(ofull(c - 1), (c - 1) >> 1, WD_DC_OUT)) break;
+                ptx::tc_fence_after_sync();
+            }
             constexpr uint32_t IDS = ptx::idesc_bf16_f32(128, 128, 0, 0), IDO = ptx::idesc_bf16_f32(128, D, 0, 1);
             mma<IDS, false>(tmem, qd, kd);
 #pragma unroll
