@@ -177,12 +177,14 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
+def _dtype_code(t) -> int:
+    """The library's code of a tensor's dtype, or of a dtype."""
+    dtype = getattr(t, "dtype", t)
+    if dtype == torch.float32:
         return F32
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return BF16
-    raise TypeError(f"unsupported dtype {t.dtype} (float32 or bfloat16)")
+    raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
 
 
 def _geom(T, Hg, Wg, block_frames, rope_split, theta, eps) -> Geom:
@@ -649,7 +651,7 @@ def _handle(stream):
 
 def decay_workspace_size(B: int, H: int, N: int, d: int, dtype: torch.dtype = torch.bfloat16) -> int:
     """Workspace bytes of decay_prefill for this shape (at most 16: it needs none)."""
-    n = int(lib.blin_decay_workspace_size(B, H, N, d, BF16 if dtype == torch.bfloat16 else F32))
+    n = int(lib.blin_decay_workspace_size(B, H, N, d, _dtype_code(dtype)))
     if n == 0:
         raise ValueError("invalid shape for blin_decay_prefill: " + lib.blin_last_error().decode())
     return n

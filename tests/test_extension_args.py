@@ -25,6 +25,13 @@ def test_dimensions_beyond_32_bits_are_refused():
             blin.decay_step(q, q, q, torch.zeros(1), torch.zeros(1, 1, 64, 64), out=q)
 
 
+def test_workspace_size_of_a_type_that_the_call_does_not_take():
+    assert blin.decay_workspace_size(1, 2, 9000, 64, torch.float32) != blin.decay_workspace_size(1, 2, 9000, 64)
+    for dtype in (torch.float16, torch.float64, "bf16", None):
+        with pytest.raises(TypeError, match="dtype"):
+            blin.decay_workspace_size(1, 2, 9000, 64, dtype)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_a_pool_without_slots_is_refused(dtype):
