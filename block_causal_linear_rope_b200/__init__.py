@@ -665,7 +665,8 @@ def decay_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: 
     S_n = exp(log_decay[h]) S_{n-1} + k_n^T v_n, o_n = scale * q_n S_n.
 
     q, k, v are [B, H, N, d] views (float32 or bfloat16, d = 32, 64 or 128, d contiguous; any
-    strides that are multiples of 16 bytes), log_decay float32 [H] with entries <= 0.  `state`,
+    strides of at least d elements that are multiples of 16 bytes, so no broadcast heads),
+    log_decay float32 [H] with entries <= 0.  `state`,
     float32 [slots, H, d, d], is a pool of states the rows start from and leave their final states
     in (updated in place; None: start from zero, keep nothing).  `slots`, int32 [B], names each
     row's slot (None: row b uses slot b); a negative entry marks an idle row, whose outputs are
@@ -676,7 +677,14 @@ def decay_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: 
     calls that may run at the same time need separate ones.  With `stream` the call runs there and
     waits for nothing: what it reads must be ready on that stream; the tensors' memory is kept
     until the call has done with it.  There is no gradient: a call
-    that autograd would have to record is refused."""
+    that autograd would have to record is refused.
+
+    In bfloat16 the weighted scores are rounded to bfloat16 and the state multiplies q with 16
+    bits, which adds to the rounding of the result: 1.7e-3 to 2.1e-3 of the outputs' 2-norm, the
+    more the faster the decays, where that rounding alone is 1.7e-3.  In float32 products take 21
+    bits of each operand (4.4e-7; operands within 2^-12 of the largest float32 overflow).  States
+    are float32 either way, to 4e-7.  How a prompt is split over the device follows from the shape
+    of the batch: the same row in another batch may differ in the last bits, equal calls do not."""
     return _result(_ext.decay_prefill(q, k, v, log_decay, state, slots, lengths, scale, out, workspace, _handle(stream)))
 
 
@@ -718,6 +726,10 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, rope_split: Seque
          theta: float = 1e4, inverse: bool = False, out=None, stream=None):
     """Rotary embedding of q [B, Hq, N, d] and, in the same launch, k [B, Hk, N, d] over the axes
     (t, y, x): the RoPE that prefill() and block_step() apply inside, as an operator of its own.
+    Its convention is theirs: neighbouring features (2j, 2j+1) of an axis' section turn together, by
+    p * theta^(-2j / section), so each axis has a ladder of frequencies of its own.  Pairs half a
+    head apart, or one ladder over the head cut into sections, are not covered.  theta is taken in
+    float32, as in the C interface; angles in double.
 
     Positions come from grid=(T, Hg, Wg), N = T*Hg*Wg, with frames counted from t0, or from
     `positions`, int32 [B, N, 3] or [N, 3] (t, y, x) of each token.  rope_split may sum to less

@@ -111,10 +111,20 @@ static bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintpt
 // split prompt has a first launch (states only) with cheaper chunks, and its second
 // one's units add up the states before them.  The split with the smallest sum is
 // taken, from sizes alone.  The costs are in chunks of the path's second launch
-// as measured on a B200: a chunk of 64 fp32 tokens takes about 7 us, one of 128
-// bf16 tokens 2 to 4 us, and a launch and a unit's start a few us either way (4
-// heads of 300 fp32 tokens: 39 us in one piece, 19 in five; 16 heads of 1024 bf16
-// tokens, d = 64: 23 us in one, 21 in four).
+// as measured on a B200 with all SMs full: a chunk of 128 bf16 tokens takes 2.0 to
+// 3.1 us at d = 32 (two CTAs to an SM), 2.0 to 2.7 at d = 64 and 4.6 to 5.0 at
+// d = 128, one of 64 fp32 tokens 8 us at d = 32 (three CTAs), 12 at d = 64 (two; one
+// alone 7) and 19 at d = 128, and a launch and a unit's start a few us either way
+// (4 heads of 300 fp32 tokens: 39 us in one piece, 19 in five; 16 heads of 1024
+// bf16 tokens, d = 64: 23 us in one, 21 in four).
+//   kMaxStates: a unit of the second launch adds up the states before it one after
+// the other, which the cost `join` states too low to hold for many of them.  One
+// head of 40000 tokens with at most 16, 32, 48 and 64 states: 164, 145, 160 and
+// 160 us at d = 128, 73, 53, 49 and 48 at d = 64 in bf16; 399, 211, 159 and 127 in
+// fp32 at d = 64, which has the most to gain from more.
+//   kMaxPieces: 32 heads of 32768 bf16 tokens, d = 128, take 440, 431, 404 and 404
+// us with at most 1, 2, 4 and 8 pieces to a segment.
+//   kSms: a part with fewer SMs gets a worse split, not a wrong one.
 static constexpr int kSms = 148, kMaxStates = 32, kMaxPieces = 4;
 struct Split {
     int nseg, seg, npiece, piece;

@@ -20,26 +20,29 @@
 // running sums towards zero).
 //
 // Roles: a TMA producer thread, two MMA issuing threads (scores and outputs,
-// state), warpgroups that weight the scores (TMEM -> registers -> P as bf16 over
-// the scores in TMEM), that weight and split the values (shared memory -> shared
+// state), warpgroups that weight the scores (TMEM -> registers -> P as bf16
+// in TMEM), that weight and split the values (shared memory -> shared
 // memory), and that own the state and the outputs.  They hand over through
 // mbarriers; every wait is bounded.
 //
 // Why 128 tokens: the scores fill the 128 lanes of one product.  A token then
-// costs (256 + 5 d) d multiply-adds, 0.04 ns of the tensor cores at d = 64 and
-// 0.14 at d = 128, where its 8 d bytes cost the memory 0.08 and 0.16.  Why one
+// costs (256 + 5 d) d multiply-adds, 0.038 ns of the tensor cores at d = 64 and
+// 0.12 at d = 128 (4096 a cycle and SM, 1.6 GHz), where its 8 d bytes cost the
+// memory 0.08 and 0.16.  Why one
 // head per CTA: the state then never leaves the registers, and K, V, Q and O
 // cross the memory once.
 //
-// Measured on a B200, sustained: 4 x 32 heads of 32760 tokens, d = 64: 577 us
-// (3.7 TB/s); 32 heads of 32768, d = 128: 468 us; 70 heads of 32760, d = 32:
-// 241 us.  What bounds it: a chunk takes 3700 cycles of an SM at d = 64 (about 8000
-// at d = 128, 3600 for two CTAs at d = 32), the round of score product, weights and
-// value product that one score buffer allows (two made each chunk's tiles stay
-// longer in the landing ring and were slower, 528 against 511 us), at 43% tensor
-// and 42 to 49% issue utilisation; and the card's power: it runs at its 1000 W limit at
-// 1.55 to 1.75 GHz (a plain copy of random data alone takes 997 W at 6.4 TB/s),
-// so that less work per chunk shows as a higher clock, not as fewer cycles.  M =
+// Measured on B200s, sustained (the range of three runs on different cards): 4 x
+// 32 heads of 32760 tokens, d = 64: 552 to 580 us (3.7 to 3.9 TB/s); 32 heads of
+// 32768, d = 128: 452 to 471 us; 70 heads of 32760, d = 32: 236 to 247 us.  What
+// bounds it: a chunk takes 3700 cycles of an SM at d = 64 (about 8000 at d = 128,
+// 4600 for two CTAs at d = 32), the round of score product, weights and value
+// product that one score buffer allows (two, tried in an earlier form of this
+// kernel, made each chunk's tiles stay longer in the landing ring: 528 us where
+// that form took 511), at 37 to 44% tensor and 42 to 50% issue utilisation; and the
+// card's power: it runs at its 1000 W limit at 1.55 to 1.75 GHz (a plain copy of
+// random data alone takes 997 W at 6.4 TB/s), so that less work per chunk shows
+// as a higher clock, not as fewer cycles.  M =
 // 64 state products at d <= 64 (d = 32 repeats its 32 features by a leading byte
 // offset of 0, and the threads of each copy take half of the columns) serve that.
 #pragma once

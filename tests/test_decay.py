@@ -3,8 +3,9 @@
 Tolerances.  Every output is a sum of products; with `A` the same sum over absolute values
 (the oracle on |q|, |k|, |v|), a chain of n fp32 roundings is off by at most n 2^-24 A.
   fp32: at most d + 2 C + 16 roundings a term (C = 128 tokens of a chunk): (d + 272) 2^-24 A.
-  bf16 outputs: scores and the state are rounded to bf16 for the tensor cores and the result once
-    more, each by at most 2^-8 of the rounded value: 2^-8 (A + |o|) on top of the fp32 bound.  As
+  bf16 outputs: scores are rounded to bf16 for the tensor cores (the state to two bf16 parts, 2^-16)
+    and the result once more, each by at most 2^-8 of the rounded value: 2^-8 (A + |o|) on top of the
+    fp32 bound holds for any share of the state (test_decay_parts bounds that share closely).  As
     these roundings are unrelated, their 2-norms add in quadrature: below 2^-8 of the output's (each
     rounding's is about 2^-8 / sqrt(3) of what it rounds, and the two parts are no larger than the
     sum where they are unrelated); twice that is allowed.
