@@ -143,6 +143,8 @@ class _NoExtension:
         self._why = why
 
     def __getattr__(self, name):
+        if name.startswith("__"):  # what inspection asks of any object
+            raise AttributeError(name)
         raise ImportError(self._why)
 
 
@@ -158,8 +160,9 @@ def _load_ext():
     except ImportError as e:  # unresolved symbols: of another torch or Python, or of an older library
         return _NoExtension(f"{path} does not load ({e}): {rebuild}")
     have = "torch {}, Python {}.{}".format(re.match(r"[\d.]*\d", torch.__version__)[0], *sys.version_info)
-    if ext.built_for != have:
-        return _NoExtension(f"{path} was built for {ext.built_for}, but this is {have}: {rebuild}")
+    built = getattr(ext, "built_for", "a version that it does not tell")
+    if built != have:
+        return _NoExtension(f"{path} was built for {built}, but this is {have}: {rebuild}")
     return ext
 
 

@@ -4,6 +4,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 import pytest
 
@@ -27,6 +28,7 @@ for call in (lambda: blin.rope(q, rope_split=(8, 12, 12), grid=(1, 2, 2)), lambd
         print("refused:", e)
     except (TypeError, ValueError) as e:
         print("there:", e)
+assert not hasattr(blin._ext, "__wrapped__")
 """
 
 
@@ -60,6 +62,16 @@ def test_an_extension_of_another_torch_is_not_called(tmp_path):
     assert all(line.startswith("there:") for line in run(where))
     lines = run(where, "1.2.3+cu128")
     assert len(lines) == 3 and all("built for torch" in line and "this is torch 1.2.3" in line for line in lines)
+
+
+def test_an_extension_that_does_not_tell_its_versions_is_not_called(tmp_path):
+    """As one that was built from older sources."""
+    src, so = tmp_path / "old.c", tmp_path / "old.so"
+    src.write_text('#include <Python.h>\nstatic struct PyModuleDef m = {PyModuleDef_HEAD_INIT, "_blin_torch", 0, -1, 0};\n'
+                   "PyMODINIT_FUNC PyInit__blin_torch(void) { return PyModule_Create(&m); }\n")
+    subprocess.check_call(["gcc", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], str(src), "-o", str(so)])
+    lines = run(package(tmp_path, so.read_bytes()))
+    assert len(lines) == 3 and all("refused:" in line and "does not tell" in line for line in lines)
 
 
 def test_the_extension_is_built_again_for_another_torch(tmp_path, monkeypatch):
