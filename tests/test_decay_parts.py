@@ -147,7 +147,7 @@ def test_outputs_carry_both_parts_of_the_state(blin, N, split, d):
 PIECES = [("bf16", 32, 3, 33, 1536, 768, 2, 384), ("bf16", 64, 2, 25, 1536, 768, 2, 384),
           ("bf16", 128, 3, 10, 2176, 768, 4, 384), ("f32", 32, 8, 8, 448, 128, 6, 64), ("f32", 64, 2, 19, 512, 128, 6, 64),
           ("f32", 128, 2, 11, 448, 128, 6, 64)]
-SORTED = [("bf16", 32, 10, 30, 9216, 3072, 4, 1536), ("bf16", 64, 5, 30, 9216, 3072, 4, 1536),
+SORTED = [("bf16", 32, 10, 30, 9856, 3328, 4, 1664), ("bf16", 64, 5, 30, 9856, 3328, 4, 1664),
           ("bf16", 128, 5, 10, 13952, 2816, 8, 1408), ("f32", 32, 5, 30, 320, 64, 4, 64), ("f32", 64, 10, 10, 320, 64, 4, 64),
           ("f32", 128, 10, 5, 320, 64, 4, 64), ("f32", 64, 20, 3, 576, 64, 8, 64)]
 # and shapes of one piece a segment, with fewer rows
